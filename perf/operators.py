@@ -85,7 +85,7 @@ def _draw(rng):
     D, Hkv, G = rng.choice([64, 80, 96, 128, 128, 192, 256]), rng.choice([1, 2, 4, 8, 12]), rng.choice([1, 2, 3, 4, 6, 7, 8, 12, 16, 20])
     cache = rng.choice([BF16, BF16, E4M3])
     B = _log(rng, 1, 256)
-    most = min(131071, (1 << 28) // (B * Hkv * D))  # keys of the padded batch: 2^28 numbers at most
+    most = min(131071, (1 << (28 if G <= 8 else 27)) // (B * Hkv * D))  # numbers in the keys of the padded batch
     length = _log(rng, 1, max(1, most))
     window = _log(rng, 1, length) if rng.random() < 0.25 else 0
     return dict(op=op, B=B, length=length, ragged=rng.random() < 0.7, Hq=Hkv * G, Hkv=Hkv, D=D, page=rng.choice([8, 16, 16, 24, 32, 64, 128]),
