@@ -108,7 +108,14 @@ const char *moe_last_error(void);
 /* ---------------------------------------------------------------- enums */
 enum {
     MOE_DTYPE_F32 = 0,      /* activations in fp32                             */
-    MOE_DTYPE_BF16 = 1      /* activations in bfloat16                         */
+    MOE_DTYPE_BF16 = 1,     /* activations in bfloat16; a key-value cache too  */
+    MOE_DTYPE_E4M3 = 2      /* a key-value cache in 8-bit floating point (4
+                               exponent, 3 mantissa bits, no infinity)         */
+};
+
+enum {
+    MOE_SCORE_SOFTMAX = 0,  /* an expert's score: softmax over all E logits    */
+    MOE_SCORE_SIGMOID = 1   /* or the sigmoid of its own logit                 */
 };
 
 enum {
@@ -224,6 +231,121 @@ int moe_prerouter_head(const moe_head_desc *hd, const void *x, int x_dtype,
  * K == E).  1 <= K <= 16, K <= E <= 1024. */
 int moe_topk_route(const float *logits, int T, int E, int K, int32_t *idx,
                    float *w, float *margin, cudaStream_t stream);
+
+/* Routing by scores.  For one token with logits z [E]:
+ *   s_e = softmax(z)_e or sigmoid(z_e);  c_e = s_e + bias_e (the balance bias
+ *   moves the choice, never the weight);
+ *   the experts stand in n_group groups of E / n_group consecutive ones; a
+ *   group's score is the sum of its group_best (1 or 2) largest c; the
+ *   keep_group groups of largest score stay (ties: the lower group);
+ *   idx = the K largest c of the kept groups, ordered by (c descending, index
+ *   ascending);  w_k = factor * s_idx[k] / sum_j s_idx[j] (renorm), or
+ *   factor * s_idx[k].
+ * moe_topk_route (softmax over the kept logits alone) is renorm = 1 with
+ * softmax scores, one group and no bias.
+ * A logit of -inf or NaN turns its expert off: it scores 0, its c is -inf,
+ * so it comes after every expert that is on (then by index) and its weight
+ * is 0; a row with nothing on gets weights 0 and valid indices.  A logit of
+ * +inf has sigmoid 1, and shares softmax's whole mass with the other +inf. */
+typedef struct {
+    int E;                    /* experts, 1 .. 1024                           */
+    int K;                    /* chosen, 1 .. 16, <= keep_group * E / n_group */
+    int score;                /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID       */
+    int n_group;              /* divides E; 1 .. 32 (1: no groups)            */
+    int keep_group;           /* 1 .. n_group                                 */
+    int group_best;           /* 1 or 2; 2 needs two experts in a group       */
+    int renorm;               /* weights divided by their sum                 */
+    float factor;
+    const float *bias;        /* [E], or NULL (zero)                          */
+} moe_route_desc;
+
+/* idx int32 [T][K], w fp32 [T][K] from logits [T][E] in logits_dtype (F32 or
+ * BF16), rows `stride` elements apart (>= E).  Scores and sums in fp32; the
+ * same inputs give the same bits. */
+int moe_scored_route(const moe_route_desc *rd, const void *logits, int logits_dtype,
+                     size_t stride, int T, int32_t *idx, float *w, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- cache */
+/* A paged key-value cache of one layer: n_pages pages of `page` tokens.  Page
+ * p's keys are [Hkv][page][D] at k + p * page_stride bytes, its values
+ * the same at v + p * page_stride, so a page's keys of one head are
+ * contiguous, and k and v may be two arrays or the halves of one page blob.
+ * A slot is a token's place in the cache: page * (size of a page) + offset.
+ * In E4M3 a stored number stands for itself times its head's scale. */
+typedef struct {
+    int n_pages;              /* n_pages * page < 2^31                        */
+    int page;                 /* tokens of a page, 1 .. 65536                 */
+    int Hkv;                  /* key-value heads                              */
+    int D;                    /* head size, a multiple of 16, 16 .. 256       */
+    int dtype;                /* MOE_DTYPE_BF16 or MOE_DTYPE_E4M3             */
+    void *k, *v;              /* 16-byte aligned                              */
+    size_t page_stride;       /* bytes, a multiple of 16, >= Hkv * page * D
+                                 numbers                                      */
+    const float *k_scale;     /* E4M3: [Hkv] fp32 on the device, or NULL (1)  */
+    const float *v_scale;
+} moe_kv_desc;
+
+/* Block tables and slots of one scheduler step, built on the GPU.
+ * R requests (0 .. 16384); request r holds seq_len[r] tokens in the cache,
+ * whose pages are block_table[r][0 .. ceil(seq_len / page) - 1].  new_len[r]
+ * >= 0: the step adds that many tokens; -1: the request has ended, and its
+ * pages go back.  Free pages stand in a ring [n_pages] of page ids:
+ * pool[0] is the place of the first free one, pool[1] their count.
+ * New pages are taken in order of requests from the ring's front and
+ * appended to the rows of block_table; returned pages go behind its end (they
+ * are free from the next call on).  The call writes
+ *   block_table, ring  only their new entries;
+ *   seq_out [R]        seq_len + new_len, 0 for an ended request (not
+ *                      seq_len itself);
+ *   first [R + 1]      the first new token of each request, then their count;
+ *   slots [cap]        the new tokens' slots in order of requests, then -1;
+ *   places [cap]       their places in their requests, then 0;
+ *   pool_out [2]       the ring's state after the step (not pool);
+ *   status [1]         MOE_OK; MOE_ENOSPACE when the free pages, a row of
+ *                      max_blocks entries or cap do not suffice; MOE_EINVAL
+ *                      for a negative length, a new_len below -1, or a pool or
+ *                      length outside its range.  Then nothing is taken:
+ *                      seq_out = seq_len, first and places 0, slots -1,
+ *                      pool_out = pool.
+ * A page id outside [0, n_pages) gives slots of -1.  page as in moe_kv_desc;
+ * n_pages * page < 2^31; all arrays int32 on the device. */
+int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R, int32_t *block_table,
+                int max_blocks, int page, int32_t *ring, int n_pages, const int32_t *pool,
+                int32_t *seq_out, int32_t *first, int32_t *slots, int32_t *places, int cap,
+                int32_t *pool_out, int32_t *status, cudaStream_t stream);
+
+/* Stores the keys and values of N tokens, [N][Hkv][D] in x_dtype (F32 or
+ * BF16), tokens k_stride / v_stride elements apart (parts of a fused
+ * projection; 16-byte multiples), at their slots.  A slot outside the cache
+ * is skipped.  BF16 rounds to nearest even; E4M3 stores x / scale rounded to
+ * nearest even, at most +-448 in size (NaN stays NaN).  Two tokens with one
+ * slot leave either. */
+int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const void *v,
+                  size_t v_stride, int x_dtype, const int32_t *slots, int N,
+                  cudaStream_t stream);
+
+/* Attention of one new token of each of B requests over the cache:
+ *   x_i = scale * q . k_i,  i over the last min(len, window) of the request's
+ *   len = seq_len[b] tokens (window 0: all);  out = sum softmax(x)_i v_i,
+ *   lse = log sum exp(x_i)  (natural; lets parts over other keys be joined).
+ * Query head h reads key head h / (Hq / Hkv).  q and out [B][Hq][D] in
+ * q_dtype (F32 or BF16), rows q_stride / out_stride elements apart (16-byte
+ * multiples); lse fp32 [B][Hq], or NULL.  block_table [B][max_blocks].
+ * A request of length <= 0 has out 0 and lse -inf.  Whatever stands in the
+ * cache behind a request's length is without effect.  A page id outside
+ * [0, n_pages), or a length above max_blocks * page, is never read through:
+ * that request's out and lse are NaN.
+ * Scores, statistics and sums in fp32; products on the tensor cores from
+ * numbers split so that an fp32 q and the softmax's weights keep fp32's
+ * accuracy (with a BF16 result at least 2^-11 before it is rounded).
+ * The same inputs give the same bits on the same device.
+ * ws: moe_paged_attention_workspace_bytes() bytes, 256-byte aligned, no
+ * clearing needed. */
+size_t moe_paged_attention_workspace_bytes(const moe_kv_desc *kv, int B, int Hq);
+int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_dtype, size_t q_stride,
+                        int B, int Hq, const int32_t *seq_len, const int32_t *block_table,
+                        int max_blocks, float scale, int window, void *out, size_t out_stride,
+                        float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- experts */
 typedef struct {

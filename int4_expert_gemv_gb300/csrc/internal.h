@@ -91,4 +91,8 @@ int num_sms();
 // Validation of a decode-stack descriptor shared by the decode-step paths.
 int check_decode_stack(const moe_stack_desc *sd);
 
+
+// Validation of a cache descriptor shared by its calls.
+int check_kv(const moe_kv_desc *kv, const char *who);
+
 }  // namespace moe

@@ -1,0 +1,358 @@
+// kv.cu -- the paged key-value cache around the decode attention: the page
+// plan of a scheduler step (block tables, slots, free pages) and the append of
+// new keys and values.
+//
+// Plan.  With b_r = ceil(len_r / page) blocks held, a_r = ceil((len_r + new_r)
+// / page) needed and exclusive sums over the requests of new_r, a_r - b_r and
+// the returned b_r, every output is a function of its own place: token i
+// belongs to the request r with first_r <= i < first_{r+1}, stands at place
+// len_r + i - first_r, and its block is either in the table already or the
+// (needed_r + block - b_r)-th free page.  So no CTA waits for another: each
+// makes the three sums for itself (R <= 16384 lengths, a few kB out of L2)
+// and then takes its share of the tokens, the new blocks and the returned
+// pages.  A second launch for the sums, or a grid barrier, would cost more
+// than repeating them.
+#include <algorithm>
+
+#include <cuda_fp8.h>
+
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanParams {
+    const int32_t *seq, *add;
+    int R;
+    int32_t *table;
+    int max_blocks;
+    FastDiv page;
+    int32_t *ring;
+    int n_pages;
+    const int32_t *pool;
+    int32_t *seq_out, *first, *slots, *places;
+    int cap;
+    int32_t *pool_out, *status;
+};
+
+// Last r with sum[r] <= i, for i below sum[R]: the request that owns item i.
+__device__ __forceinline__ int owner(const int32_t *sum, int R, int i) {
+    int lo = 0, n = R;
+    while (n > 1) {
+        const int half = n >> 1;
+        if (sum[lo + half] <= i) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int wrap(int64_t i, int n) { return (int)(i < n ? i : i - n); }
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams p) {
+    extern __shared__ int32_t sums[];               // [3][R + 1]
+    __shared__ int64_t part[3][kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.R;
+    int32_t *s_new = sums, *s_need = sums + R + 1, *s_gone = sums + 2 * (R + 1);
+    const int page = p.page.d;
+    const int head = p.pool[0], n_free = p.pool[1];
+    const int64_t room = (int64_t)p.max_blocks * page;
+
+    // this thread's run of requests
+    const int run = (R + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = min(R, tid * run), r1 = min(R, r0 + run);
+    bool invalid = head < 0 || head >= p.n_pages || n_free < 0 || n_free > p.n_pages;
+    bool nospace = false;
+    int64_t sum[3] = {0, 0, 0};
+    for (int r = r0; r < r1; r++) {
+        const int len = p.seq[r], add = p.add[r];
+        if (len < 0 || len > room || add < -1) {
+            invalid = true;
+            continue;
+        }
+        const int have = p.page.ceil(len);
+        if (add < 0) {
+            sum[2] += have;
+        } else if ((int64_t)len + add > room || (int64_t)len + add > INT32_MAX) {
+            nospace = true;
+        } else {
+            sum[0] += add;
+            sum[1] += p.page.ceil(len + add) - have;
+        }
+    }
+    int64_t upto[3];
+#pragma unroll
+    for (int j = 0; j < 3; j++) {
+        int64_t v = sum[j];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        upto[j] = v - sum[j];
+        if (lane == 31) part[j][warp] = v;
+    }
+    __syncthreads();
+    int64_t total[3] = {0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 3; j++)
+        for (int w = 0; w < kPlanWarps; w++) {
+            if (w == warp) upto[j] += total[j];
+            total[j] += part[j][w];
+        }
+    nospace |= total[0] > p.cap || total[1] > n_free;
+    // more pages held than there are: the tables and the ring contradict each other
+    invalid |= n_free + total[2] > p.n_pages;
+    const int bad_i = __syncthreads_or(invalid), bad_s = __syncthreads_or(nospace);
+    const int step = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;
+    if (bad_i || bad_s) {                           // the same answer in every CTA
+        for (int r = me; r < R; r += step) p.seq_out[r] = p.seq[r];
+        for (int r = me; r <= R; r += step) p.first[r] = 0;
+        for (int i = me; i < p.cap; i += step) {
+            p.slots[i] = -1;
+            p.places[i] = 0;
+        }
+        if (me == 0) {
+            p.pool_out[0] = head;
+            p.pool_out[1] = n_free;
+            p.status[0] = bad_i ? MOE_EINVAL : MOE_ENOSPACE;
+        }
+        return;
+    }
+    for (int r = r0; r < r1; r++) {
+        const int len = p.seq[r], add = p.add[r];
+        const int have = p.page.ceil(len);
+        s_new[r] = (int)upto[0];
+        s_need[r] = (int)upto[1];
+        s_gone[r] = (int)upto[2];
+        if (blockIdx.x == 0) {
+            p.first[r] = (int)upto[0];
+            p.seq_out[r] = add < 0 ? 0 : len + add;
+        }
+        if (add < 0) {
+            upto[2] += have;
+        } else {
+            upto[0] += add;
+            upto[1] += p.page.ceil(len + add) - have;
+        }
+    }
+    const int n_new = (int)total[0], n_need = (int)total[1], n_gone = (int)total[2];
+    if (me == 0) {
+        p.first[R] = n_new;
+        p.pool_out[0] = wrap((int64_t)head + n_need, p.n_pages);
+        p.pool_out[1] = n_free - n_need + n_gone;
+        p.status[0] = MOE_OK;
+    }
+    __syncthreads();
+    // new blocks
+    for (int j = me; j < n_need; j += step) {
+        const int r = owner(s_need, R, j);
+        const int b = p.page.ceil(p.seq[r]) + j - s_need[r];
+        p.table[(size_t)r * p.max_blocks + b] = p.ring[wrap((int64_t)head + j, p.n_pages)];
+    }
+    // returned pages: behind the free part, where no page is being taken
+    for (int j = me; j < n_gone; j += step) {
+        const int r = owner(s_gone, R, j);
+        p.ring[(int)(((int64_t)head + n_free + j) % p.n_pages)] =
+            p.table[(size_t)r * p.max_blocks + j - s_gone[r]];
+    }
+    // slots and places
+    for (int i = me; i < p.cap; i += step) {
+        int slot = -1, place = 0;
+        if (i < n_new) {
+            const int r = owner(s_new, R, i);
+            const int len = p.seq[r];
+            place = len + i - s_new[r];
+            const int b = p.page.div(place), have = p.page.ceil(len);
+            const int id = b < have ? p.table[(size_t)r * p.max_blocks + b]
+                                    : p.ring[wrap((int64_t)head + s_need[r] + b - have, p.n_pages)];
+            if ((unsigned)id < (unsigned)p.n_pages) slot = id * page + place - b * page;
+        }
+        p.slots[i] = slot;
+        p.places[i] = place;
+    }
+}
+
+// ---------------------------------------------------------------- append
+struct AppendParams {
+    const void *k, *v;
+    size_t k_stride, v_stride;      // elements
+    const int32_t *slots;
+    int N, n_slots, D;
+    FastDiv page, row, head;        // chunks of 8 numbers: of a token, of a head
+    uint8_t *ck, *cv;
+    size_t page_stride;
+    const float *k_scale, *v_scale;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const void *x, size_t i, float *f);
+template <>
+__device__ __forceinline__ void load8<float>(const void *x, size_t i, float *f) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const void *x, size_t i, float *f) {
+    const uint4 a = ld_stream16(static_cast<const __nv_bfloat16 *>(x) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+
+// Eight numbers stored: bf16 rounded to nearest even, or e4m3 of x / scale,
+// the quotient rounded once and clamped to the largest number.
+__device__ __forceinline__ void store8_bf16(uint8_t *dst, const float *f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8_e4m3(uint8_t *dst, const float *f, float scale) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 x = make_float2(__fdiv_rn(f[2 * j], scale), __fdiv_rn(f[2 * j + 1], scale));
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+        w[j / 2] |= b << (16 * (j & 1));
+    }
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+}
+
+template <typename X, bool E4M3>
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
+    const int64_t total = (int64_t)p.N * p.row.d;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < total; c += (int64_t)gridDim.x * 256) {
+        const int n = (int)(c / p.row.d), in = (int)(c - (int64_t)n * p.row.d);
+        const int slot = p.slots[n];
+        if ((unsigned)slot >= (unsigned)p.n_slots) continue;
+        const int h = p.head.div(in), i = in - h * p.head.d;
+        const int pg = p.page.div(slot), off = slot - pg * p.page.d;
+        const size_t at = (size_t)pg * p.page_stride +
+                          (((size_t)h * p.page.d + off) * p.D + 8 * i) * (E4M3 ? 1 : 2);
+        float a[8], b[8];
+        load8<X>(p.k, (size_t)n * p.k_stride + 8 * in, a);
+        load8<X>(p.v, (size_t)n * p.v_stride + 8 * in, b);
+        if (E4M3) {
+            store8_e4m3(p.ck + at, a, p.k_scale ? p.k_scale[h] : 1.0f);
+            store8_e4m3(p.cv + at, b, p.v_scale ? p.v_scale[h] : 1.0f);
+        } else {
+            store8_bf16(p.ck + at, a);
+            store8_bf16(p.cv + at, b);
+        }
+    }
+}
+
+}  // namespace
+
+int check_kv(const moe_kv_desc *kv, const char *who) {
+    if (kv == nullptr) return fail(MOE_EINVAL, "%s: cache descriptor is NULL", who);
+    if (kv->n_pages < 1 || kv->page < 1 || kv->page > 65536 || kv->Hkv < 1 || kv->Hkv > 65536 ||
+        kv->D < 16 || kv->D > 256 || kv->D % 16)
+        return fail(MOE_EINVAL, "%s: n_pages=%d page=%d Hkv=%d D=%d (page 1..65536, Hkv 1..65536, "
+                                "D a multiple of 16 up to 256)", who, kv->n_pages, kv->page,
+                    kv->Hkv, kv->D);
+    if ((int64_t)kv->n_pages * kv->page >= (int64_t)1 << 31)
+        return fail(MOE_EUNSUPPORTED, "%s: %d pages of %d tokens (need fewer than 2^31 slots)", who,
+                    kv->n_pages, kv->page);
+    if (kv->dtype != MOE_DTYPE_BF16 && kv->dtype != MOE_DTYPE_E4M3)
+        return fail(MOE_EINVAL, "%s: cache dtype=%d (need MOE_DTYPE_BF16 or MOE_DTYPE_E4M3)", who,
+                    kv->dtype);
+    if (!kv->k || !kv->v || reinterpret_cast<uintptr_t>(kv->k) % 16 ||
+        reinterpret_cast<uintptr_t>(kv->v) % 16)
+        return fail(MOE_EINVAL, "%s: NULL or misaligned k/v", who);
+    const size_t need = (size_t)kv->Hkv * kv->page * kv->D * (kv->dtype == MOE_DTYPE_E4M3 ? 1 : 2);
+    if (kv->page_stride < need || kv->page_stride % 16)
+        return fail(MOE_EINVAL, "%s: page_stride %zu (need >= %zu, multiple of 16)", who,
+                    kv->page_stride, need);
+    if (kv->dtype != MOE_DTYPE_E4M3 && (kv->k_scale || kv->v_scale))
+        return fail(MOE_EINVAL, "%s: scales with a bf16 cache", who);
+    if (reinterpret_cast<uintptr_t>(kv->k_scale) % 4 || reinterpret_cast<uintptr_t>(kv->v_scale) % 4)
+        return fail(MOE_EINVAL, "%s: misaligned scales", who);
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+static bool off4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
+
+extern "C" int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R,
+                           int32_t *block_table, int max_blocks, int page, int32_t *ring,
+                           int n_pages, const int32_t *pool, int32_t *seq_out, int32_t *first,
+                           int32_t *slots, int32_t *places, int cap, int32_t *pool_out,
+                           int32_t *status, cudaStream_t stream) {
+    if (R < 0 || cap < 0 || max_blocks < 1 || page < 1 || page > 65536 || n_pages < 1)
+        return fail(MOE_EINVAL, "kv_plan: R=%d cap=%d max_blocks=%d page=%d n_pages=%d", R, cap,
+                    max_blocks, page, n_pages);
+    if (R > kMaxPlanRequests || (int64_t)n_pages * page >= (int64_t)1 << 31)
+        return fail(MOE_EUNSUPPORTED, "kv_plan: R=%d (at most %d), %d pages of %d tokens (fewer than "
+                                      "2^31 slots)", R, kMaxPlanRequests, n_pages, page);
+    if (!ring || !pool || !first || !pool_out || !status || (cap > 0 && (!slots || !places)) ||
+        (R > 0 && (!seq_len || !new_len || !block_table || !seq_out)))
+        return fail(MOE_EINVAL, "kv_plan: NULL pointer");
+    if (off4(seq_len) || off4(new_len) || off4(block_table) || off4(ring) || off4(pool) ||
+        off4(seq_out) || off4(first) || off4(slots) || off4(places) || off4(pool_out) || off4(status))
+        return fail(MOE_EINVAL, "kv_plan: misaligned pointer");
+    if ((R > 0 && (seq_out == seq_len || first == seq_len || first == new_len)) || pool_out == pool)
+        return fail(MOE_EINVAL, "kv_plan: an output is an input");
+    const PlanParams p{seq_len, new_len, R, block_table, max_blocks, FastDiv(page), ring, n_pages,
+                       pool, seq_out, first, slots, places, cap, pool_out, status};
+    const size_t smem = 3 * (size_t)(R + 1) * sizeof(int32_t);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return fail(MOE_ECUDA, "kv_plan: %s", cudaGetErrorString(e));
+    }
+    const int want = (cap + 1023) / 1024 + (R + 15) / 16;
+    kv_plan_kernel<<<std::max(1, std::min(want, num_sms())), kPlanThreads, smem, stream>>>(p);
+    return check_launch("kv_plan_kernel");
+}
+
+extern "C" int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const void *v,
+                             size_t v_stride, int x_dtype, const int32_t *slots, int N,
+                             cudaStream_t stream) {
+    if (int rc = check_kv(kv, "kv_append")) return rc;
+    if (N < 0) return fail(MOE_EINVAL, "kv_append: N=%d", N);
+    if (x_dtype != MOE_DTYPE_F32 && x_dtype != MOE_DTYPE_BF16)
+        return fail(MOE_EINVAL, "kv_append: x_dtype=%d", x_dtype);
+    if (N == 0) return MOE_OK;
+    const size_t row = (size_t)kv->Hkv * kv->D, elt = x_dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (!k || !v || !slots || reinterpret_cast<uintptr_t>(k) % 16 ||
+        reinterpret_cast<uintptr_t>(v) % 16 || off4(slots))
+        return fail(MOE_EINVAL, "kv_append: NULL or misaligned k/v/slots");
+    if ((N > 1 && (k_stride < row || v_stride < row)) || k_stride * elt % 16 || v_stride * elt % 16)
+        return fail(MOE_EINVAL, "kv_append: strides %zu / %zu (need >= %zu numbers, 16-byte "
+                                "multiples)", k_stride, v_stride, row);
+    const AppendParams p{k, v, k_stride, v_stride, slots, N, kv->n_pages * kv->page, kv->D,
+                         FastDiv(kv->page), FastDiv((int)(row / 8)), FastDiv(kv->D / 8),
+                         static_cast<uint8_t *>(kv->k), static_cast<uint8_t *>(kv->v),
+                         kv->page_stride, kv->k_scale, kv->v_scale};
+    const int64_t total = (int64_t)N * (int64_t)(row / 8);
+    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 8);
+    const bool f8 = kv->dtype == MOE_DTYPE_E4M3;
+    if (x_dtype == MOE_DTYPE_F32) {
+        if (f8) kv_append_kernel<float, true><<<grid, 256, 0, stream>>>(p);
+        else kv_append_kernel<float, false><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (f8) kv_append_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
+        else kv_append_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(p);
+    }
+    return check_launch("kv_append_kernel");
+}

@@ -17,7 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECUDA, MOE_ETIMEOUT, MOE_ENOSPACE = range(6)
-MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_E4M3 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_PREC_AFFINE4, MOE_PREC_FP16 = 4, 16
 
 _lock = threading.Lock()
@@ -65,6 +66,18 @@ class ChainInfo(C.Structure):
                 ("ctas_a", C.c_int), ("ctas_b", C.c_int), ("coresident", C.c_int)]
 
 
+class RouteDesc(C.Structure):
+    _fields_ = [("E", C.c_int), ("K", C.c_int), ("score", C.c_int), ("n_group", C.c_int),
+                ("keep_group", C.c_int), ("group_best", C.c_int), ("renorm", C.c_int),
+                ("factor", C.c_float), ("bias", C.c_void_p)]
+
+
+class KVDesc(C.Structure):
+    _fields_ = [("n_pages", C.c_int), ("page", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+                ("dtype", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("page_stride", C.c_size_t), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
 # ------------------------------------------------------------------ loading
 def lib():
     global _lib
@@ -93,6 +106,12 @@ def lib():
                 "moe_prerouter_head_workspace_bytes": (S, [C.POINTER(HeadDesc), I]),
                 "moe_prerouter_head": (I, [C.POINTER(HeadDesc), P, I, P, P, I, I, P, P, S, P]),
                 "moe_topk_route": (I, [P, I, I, I, P, P, P, P]),
+                "moe_scored_route": (I, [C.POINTER(RouteDesc), P, I, S, I, P, P, P]),
+                "moe_kv_plan": (I, [P, P, I, P, I, I, P, I, P, P, P, P, P, I, P, P, P]),
+                "moe_kv_append": (I, [C.POINTER(KVDesc), P, S, P, S, I, P, I, P]),
+                "moe_paged_attention_workspace_bytes": (S, [C.POINTER(KVDesc), I, I]),
+                "moe_paged_attention": (I, [C.POINTER(KVDesc), P, I, S, I, I, P, P, I, C.c_float, I,
+                                            P, S, P, P, S, P]),
                 "moe_expert_ffn_workspace_bytes": (S, [C.POINTER(ExpertsDesc), I, I]),
                 "moe_expert_ffn_int4": (I, [C.POINTER(ExpertsDesc), P, I, P, I, I, P, P, S, P]),
                 "moe_combine_residual": (I, [P, P, I, I, I, I, P, P, P, P]),
@@ -256,6 +275,62 @@ def moe_prerouter_head(hd: HeadDesc, x, cur_idx, prev_idx, K: int, T: int, logit
 def moe_topk_route(logits, T: int, E: int, K: int, idx, w, margin=None, stream=None):
     _check(lib().moe_topk_route(_ptr(logits), T, E, K, _ptr(idx), _ptr(w), _ptr(margin),
                                 _stream(stream)), "moe_topk_route")
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of a tensor whose rows are contiguous."""
+    if t.is_contiguous():
+        return t.numel() // max(1, t.shape[0])
+    inner = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != inner:
+            raise ValueError(f"rows must be contiguous: shape {tuple(t.shape)}, strides {t.stride()}")
+        inner *= n
+    return inner if t.shape[0] <= 1 else t.stride(0)
+
+
+def moe_scored_route(rd: RouteDesc, logits, T: int, idx, w, stream=None):
+    """Top-K experts by softmax or sigmoid scores with a balance bias and
+    groups; logits fp32 or bf16 [T][E], rows may be strided."""
+    _check(lib().moe_scored_route(C.byref(rd), _ptr(logits), _dtype_code(logits),
+                                  _row_stride(logits), T, _ptr(idx), _ptr(w), _stream(stream)),
+           "moe_scored_route")
+
+
+def moe_kv_plan(seq_len, new_len, R: int, block_table, max_blocks: int, page: int, ring,
+                n_pages: int, pool, seq_out, first, slots, places, cap: int, pool_out, status,
+                stream=None):
+    """Block tables, slots and places of a scheduler step's new tokens, pages
+    taken from and given back to the ring of free ones (see include/moe.h)."""
+    _check(lib().moe_kv_plan(_ptr(seq_len), _ptr(new_len), R, _ptr(block_table), max_blocks, page,
+                             _ptr(ring), n_pages, _ptr(pool), _ptr(seq_out), _ptr(first),
+                             _ptr(slots), _ptr(places), cap, _ptr(pool_out), _ptr(status),
+                             _stream(stream)), "moe_kv_plan")
+
+
+def moe_kv_append(kv: KVDesc, k, v, slots, N: int, stream=None):
+    """Keys and values of N tokens into the paged cache at their slots;
+    k, v: fp32 or bf16 [N][Hkv][D] or [N][Hkv * D], tokens may be strided."""
+    if k.dtype != v.dtype:
+        raise TypeError(f"k and v must have one type, got {k.dtype} and {v.dtype}")
+    _check(lib().moe_kv_append(C.byref(kv), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v),
+                               _dtype_code(k), _ptr(slots), N, _stream(stream)), "moe_kv_append")
+
+
+def moe_paged_attention_workspace_bytes(kv: KVDesc, B: int, Hq: int) -> int:
+    return lib().moe_paged_attention_workspace_bytes(C.byref(kv), B, Hq)
+
+
+def moe_paged_attention(kv: KVDesc, q, B: int, Hq: int, seq_len, block_table, max_blocks: int,
+                        scale: float, out, ws, lse=None, window: int = 0, stream=None):
+    """Attention of one new token per request over the paged cache; q and out
+    fp32 or bf16 (one type) [B][Hq][D], rows may be strided."""
+    if q.dtype != out.dtype:
+        raise TypeError(f"q and out must have one type, got {q.dtype} and {out.dtype}")
+    _check(lib().moe_paged_attention(C.byref(kv), _ptr(q), _dtype_code(q), _row_stride(q), B, Hq,
+                                     _ptr(seq_len), _ptr(block_table), max_blocks, scale, window,
+                                     _ptr(out), _row_stride(out), _ptr(lse), _ptr(ws), _nbytes(ws),
+                                     _stream(stream)), "moe_paged_attention")
 
 
 def moe_expert_ffn_int4(ed: ExpertsDesc, x, idx, T: int, K: int, y_slots, ws, stream=None,

@@ -1,0 +1,494 @@
+"""The paged key-value cache on the GPU (needs a GPU): the page plan against a
+plain allocator, the append against elementwise rounding, the attention of
+one new token per request against the formula in 64 bits."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+E4M3_MAX = 448.0
+
+
+@pytest.fixture(scope="module")
+def m():
+    from int4_expert_gemv_gb300 import build
+    build.build()
+    from int4_expert_gemv_gb300 import moe
+    moe.lib()
+    return moe
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------ plan
+class Plan:
+    """The plan's buffers, and its rules written out one request at a time."""
+
+    def __init__(self, R, max_blocks, page, n_pages, cap, seed=0):
+        self.R, self.mb, self.page, self.P, self.cap = R, max_blocks, page, n_pages, cap
+        self.rng = np.random.default_rng(seed)
+        self.table = np.full((R, max_blocks), -7, np.int32)
+        self.ring = self.rng.permutation(n_pages).astype(np.int32)
+        self.pool = [int(self.rng.integers(0, n_pages)), n_pages]
+        self.seq = np.zeros(R, np.int32)
+        self.dev = None
+
+    def expect(self, new):
+        """(status, outputs) of one step; the state moves on when it is 0."""
+        R, page, P, cap = self.R, self.page, self.P, self.cap
+        have = [-(-int(s) // page) for s in self.seq]
+        add = [max(0, int(n)) for n in new]
+        after = [-(-(int(s) + a) // page) for s, a in zip(self.seq, add)]
+        need = sum(a - h for a, h in zip(after, have))
+        head, free = self.pool
+        first = np.zeros(R + 1, np.int32)
+        slots, places = np.full(cap, -1, np.int32), np.zeros(cap, np.int32)
+        if max(after, default=0) > self.mb or need > free or sum(add) > cap:
+            return 5, (self.seq.copy(), first, slots, places, list(self.pool))
+        ring0, j, i, gone = self.ring.copy(), 0, 0, []
+        out = self.seq.copy()
+        for r in range(R):
+            for b in range(have[r], after[r]):
+                self.table[r, b] = ring0[(head + j) % P]
+                j += 1
+            first[r] = i
+            for t in range(int(self.seq[r]), int(self.seq[r]) + add[r]):
+                slots[i] = self.table[r, t // page] * page + t % page
+                places[i] = t
+                i += 1
+            out[r] = self.seq[r] + add[r]
+            if new[r] < 0:
+                gone += list(self.table[r, : have[r]])
+                out[r] = 0
+        first[R] = i
+        for k, g in enumerate(gone):
+            self.ring[(head + free + k) % P] = g
+        self.pool = [(head + need) % P, free - need + len(gone)]
+        self.seq = out
+        return 0, (out.copy(), first, slots, places, list(self.pool))
+
+    def upload(self):
+        self.dev = dict(table=torch.from_numpy(self.table.copy()).cuda(), ring=torch.from_numpy(self.ring.copy()).cuda(),
+                        seq=torch.from_numpy(self.seq.copy()).cuda(), pool=_ints(self.pool))
+
+    def call(self, m, new):
+        d, R = self.dev, self.R
+        fill = lambda n: torch.full((n,), 12345, dtype=torch.int32, device="cuda")  # noqa: E731
+        o = dict(seq=fill(R), first=fill(R + 1), slots=fill(self.cap), places=fill(self.cap), pool=fill(2), status=fill(1))
+        m.moe_kv_plan(d["seq"], _ints(list(new)), R, d["table"], self.mb, self.page, d["ring"], self.P, d["pool"],
+                      o["seq"], o["first"], o["slots"], o["places"], self.cap, o["pool"], o["status"])
+        got = {k: v.cpu().numpy() for k, v in o.items()}
+        d["seq"], d["pool"] = o["seq"], o["pool"]
+        return got
+
+
+def _same_step(m, plan, new):
+    st, (seq, first, slots, places, pool) = plan.expect(new)
+    got = plan.call(m, new)
+    assert got["status"][0] == st
+    assert np.array_equal(got["seq"], seq) and np.array_equal(got["first"], first)
+    assert np.array_equal(got["slots"], slots) and np.array_equal(got["places"], places)
+    assert got["pool"].tolist() == pool
+    assert np.array_equal(plan.dev["table"].cpu().numpy(), plan.table)
+    assert np.array_equal(plan.dev["ring"].cpu().numpy(), plan.ring)
+    return st
+
+
+@pytest.mark.parametrize("R,max_blocks,page,n_pages,cap", [
+    (1, 4, 16, 3, 64), (5, 9, 1, 20, 30), (33, 7, 24, 150, 700), (256, 40, 16, 5000, 4000), (1000, 3, 128, 2000, 999),
+    (600, 64, 3, 9000, 20000)])
+def test_plan_steps_follow_the_allocator(m, R, max_blocks, page, n_pages, cap):
+    """Many steps in a row: requests grow, wait, end and start again, some
+    steps ask for more than there is and change nothing."""
+    p = Plan(R, max_blocks, page, n_pages, cap, seed=R)
+    p.upload()
+    seen = set()
+    for step in range(12):
+        big = p.rng.random(R) < 0.3
+        new = np.where(big, p.rng.integers(0, 2 * page + 2, R), p.rng.integers(0, 2, R))
+        new = np.where(p.rng.random(R) < 0.15, -1, new)
+        if step % 4 != 3:                            # otherwise as drawn, too much or not
+            over = p.seq + np.maximum(new, 0) > max_blocks * page
+            new = np.where(over, -1, new)
+            room = cap
+            for r in range(R):
+                new[r] = min(new[r], room)
+                room -= max(0, new[r])
+        seen.add(_same_step(m, p, new))
+        held = [p.table[r, b] for r in range(R) for b in range(-(-int(p.seq[r]) // page))]
+        free = [p.ring[(p.pool[0] + i) % n_pages] for i in range(p.pool[1])]
+        assert sorted(held + free) == list(range(n_pages))   # every page once, always
+    assert 0 in seen
+
+
+def test_plan_refuses_what_does_not_fit(m):
+    def step(seq, new, max_blocks=4, page=8, n_pages=10, cap=40, pool=(3, 5)):
+        R = len(seq)
+        table = torch.arange(R * max_blocks, dtype=torch.int32, device="cuda").view(R, max_blocks) % n_pages
+        ring = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+        before = table.clone(), ring.clone()
+        fill = lambda n: torch.full((n,), 9, dtype=torch.int32, device="cuda")  # noqa: E731
+        so, fi, sl, pl, po, st = fill(R), fill(R + 1), fill(cap), fill(cap), fill(2), fill(1)
+        m.moe_kv_plan(_ints(list(seq)), _ints(list(new)), R, table, max_blocks, page, ring, n_pages, _ints(list(pool)), so, fi, sl, pl,
+                      cap, po, st)
+        status = int(st[0])
+        if status:
+            assert torch.equal(table, before[0]) and torch.equal(ring, before[1])
+            assert so.tolist() == list(seq) and fi.tolist() == [0] * (R + 1) and po.tolist() == list(pool)
+            assert sl.tolist() == [-1] * cap and pl.tolist() == [0] * cap
+        return status
+
+    top = 2 ** 31 - 1
+    assert step([8, 3], [1, 1]) == m.MOE_OK
+    assert step([8, 3], [25, 0]) == m.MOE_ENOSPACE            # the row
+    assert step([8, 3], [8, 8], pool=(3, 1)) == m.MOE_ENOSPACE   # the pages
+    assert step([0, 0], [20, 21]) == m.MOE_ENOSPACE           # the slots
+    assert step([0, 0], [top, top]) == m.MOE_ENOSPACE
+    assert step([8, 3], [top, -1]) == m.MOE_ENOSPACE
+    assert step([-1, 3], [0, 0]) == m.MOE_EINVAL
+    assert step([33, 3], [0, 0]) == m.MOE_EINVAL              # longer than its row
+    assert step([8, 3], [-2, 0]) == m.MOE_EINVAL
+    for pool in [(10, 5), (-1, 5), (0, 11), (0, -1)]:
+        assert step([8, 3], [0, 0], pool=pool) == m.MOE_EINVAL
+    assert step([32, 32], [-1, -1], pool=(0, 5)) == m.MOE_EINVAL  # 8 pages back into a ring with 5 of 10
+    assert step([], []) == m.MOE_OK
+
+
+def test_plan_of_no_new_tokens_and_of_many_requests(m):
+    p = Plan(16384, 2, 4, 20000, 0, seed=3)
+    p.upload()
+    assert _same_step(m, p, np.zeros(16384, np.int64)) == 0
+    p = Plan(16384, 2, 4, 20000, 16384, seed=4)
+    p.upload()
+    assert _same_step(m, p, p.rng.integers(0, 2, 16384)) == 0
+    assert _same_step(m, p, p.rng.integers(-1, 2, 16384)) == 0
+
+
+def test_plan_marks_slots_of_pages_that_do_not_exist(m):
+    one = lambda v: _ints([v])  # noqa: E731
+    table, ring = _ints([[77, -1, 0, 0]]), _ints([5, 1, 2, 3, 0])
+    so, fi, sl, pl, po, st = (_ints([0] * n) for n in (1, 2, 12, 12, 2, 1))
+    m.moe_kv_plan(one(2), one(8), 1, table, 4, 4, ring, 5, _ints([0, 5]), so, fi, sl, pl, 12, po, st)
+    assert st.tolist() == [0]
+    # places 2..3 stand in page 77, 4..7 in ring entry 5 (neither is a page), 8..9 in page 1
+    assert sl.tolist() == [-1] * 6 + [4, 5] + [-1] * 4
+    assert pl.tolist() == list(range(2, 10)) + [0] * 4
+
+
+# ------------------------------------------------------------ append
+def _desc(m, kv, scales=(None, None), split=False):
+    """kv [pages][2][Hkv][page][D], or with split two arrays [pages][Hkv][page][D]."""
+    k, v = (kv[0], kv[1]) if split else (kv[:, 0], kv[:, 1])
+    P, H, page, D = k.shape
+    elt = k.element_size()
+    return m.KVDesc(n_pages=P, page=page, Hkv=H, D=D, dtype=m.MOE_DTYPE_BF16 if elt == 2 else m.MOE_DTYPE_E4M3, k=k.data_ptr(),
+                    v=v.data_ptr(), page_stride=k.stride(0) * elt, k_scale=None if scales[0] is None else scales[0].data_ptr(),
+                    v_scale=None if scales[1] is None else scales[1].data_ptr())
+
+
+@pytest.mark.parametrize("x", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("N,H,page,D", [(1, 1, 1, 16), (7, 3, 24, 80), (130, 8, 16, 128), (65, 2, 5, 256)])
+def test_append_stores_rounded_rows_and_nothing_else(m, x, cache, N, H, page, D):
+    g = torch.Generator(device="cuda").manual_seed(N + D)
+    P = N // page + 3
+    qkv = (3 * torch.randn((N, 4 * H * D), generator=g, device="cuda"))
+    qkv[0, H * D: H * D + 8] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1e30, -1e30, 0.0, -0.0, 2.0 ** -9],
+                                            device="cuda")
+    qkv = qkv.to(x)
+    k, v = qkv[:, H * D: 2 * H * D], qkv[:, 3 * H * D:]
+    sc = (None, None)
+    if cache != torch.bfloat16:
+        sc = tuple(0.01 + 0.01 * torch.rand(H, generator=g, device="cuda") for _ in range(2))
+    bits = torch.int16 if cache == torch.bfloat16 else torch.uint8
+    kv = torch.full((P, 2, H, page, D), 77, dtype=bits, device="cuda")
+    ref = kv.clone().cpu()
+    slots = torch.randperm(P * page, generator=g, device="cuda", dtype=torch.int32)[:N].clone()
+    if N > 6:
+        slots[3], slots[5] = -1, P * page                # padding, and outside the cache
+    m.moe_kv_append(_desc(m, kv, sc), k, v, slots, N)
+    for part, t, s in ((0, k, sc[0]), (1, v, sc[1])):
+        t = t.reshape(N, H, D).float()
+        if s is not None:
+            t = (t / s[:, None]).clamp(-E4M3_MAX, E4M3_MAX)
+        t = t.to(cache).view(bits).cpu()
+        for n, slot in enumerate(slots.tolist()):
+            if 0 <= slot < P * page:
+                ref[slot // page, part, :, slot % page] = t[n]
+    got, at = kv.cpu(), kv.view(cache).float().isnan().cpu()
+    assert torch.equal(at, ref.view(cache).float().isnan())
+    assert torch.equal(got[~at], ref[~at])
+
+
+# ------------------------------------------------------------ attention
+def _attend_case(m, lens, Hq, H, D, page, q_type, cache, window=0, seed=0, split=False, pad=0, P=None, spread=1.0, table_pad=2):
+    """Runs one call on a cache whose every number behind the lengths is NaN,
+    and whose table entries behind the blocks name no page."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B = len(lens)
+    nb = [-(-max(0, n) // page) for n in lens]
+    P = P or sum(nb) + 2
+    wide = max(nb + [0]) + table_pad
+    table = torch.full((B, wide), 2 ** 30, dtype=torch.int32, device="cuda")
+    pages = torch.randperm(P, generator=g, device="cuda", dtype=torch.int32).tolist()
+    for b, n in enumerate(nb):
+        for j in range(n):
+            table[b, j] = pages.pop()
+    f8 = cache == torch.float8_e4m3fn
+    shape = (2, P, H, page, D) if split else (P, 2, H, page, D)
+    kv = torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    k, v = (kv[0], kv[1]) if split else (kv[:, 0], kv[:, 1])
+    sc = tuple(0.01 + 0.01 * torch.rand(H, generator=g, device="cuda") for _ in range(2)) if f8 else (None, None)
+    for b, n in enumerate(lens):
+        if n > 0:
+            at = torch.arange(n, device="cuda")
+            pg, off = table[b].long()[at // page], at % page
+            for part in (k, v):
+                x = torch.randn((n, H, D), generator=g, device="cuda") * spread
+                part[pg, :, off] = (x / 0.015).clamp(-E4M3_MAX, E4M3_MAX).bfloat16() if f8 else x.bfloat16()
+    kv = kv.to(cache)
+    q = torch.randn((B, Hq * D + pad), generator=g, device="cuda").to(q_type)[:, : Hq * D].view(B, Hq, D)
+    out = torch.full((B, Hq * D + pad), 5.0, dtype=q_type, device="cuda")
+    lse = torch.full((B, Hq), 5.0, device="cuda")
+    seq = _ints(list(lens))
+    desc = _desc(m, kv, sc, split)
+    ws = torch.full((m.moe_paged_attention_workspace_bytes(desc, B, Hq),), 255, dtype=torch.uint8, device="cuda")
+    return dict(kv=kv, sc=sc, q=q, out=out, o=out[:, : Hq * D].view(B, Hq, D), lse=lse, seq=seq, table=table, desc=desc, ws=ws, lens=lens,
+                Hq=Hq, H=H, D=D, page=page, window=window, split=split, scale=D ** -0.5)
+
+
+def _call(m, c, stream=None):
+    m.moe_paged_attention(c["desc"], c["q"], len(c["lens"]), c["Hq"], c["seq"], c["table"], c["table"].shape[1], c["scale"], c["o"],
+                          c["ws"], lse=c["lse"], window=c["window"], stream=stream)
+
+
+def _check(c, skip=()):
+    """The formula in 64 bits.  Bounds: with dx the error of a score (fp32
+    sums of D products, each within 2^-22 of exact, and the exponent's
+    argument in fp32), a weight is within 2 dx + 2^-20 of exact relative to
+    the weights' sum, so out within that times max |v| -- and with a 16-bit
+    result, whose weights keep 11 bits (2^-12 after rounding), 2^-12 max |v|
+    more and half a unit of bf16 -- and lse within dx + 2^-20 (1 + |lse|)."""
+    kv, D, G, page = c["kv"], c["D"], c["Hq"] // c["H"], c["page"]
+    k, v = (kv[0], kv[1]) if c["split"] else (kv[:, 0], kv[:, 1])
+    out, lse = c["o"].double(), c["lse"].double()
+    for b, n in enumerate(c["lens"]):
+        if b in skip:
+            assert out[b].isnan().all() and lse[b].isnan().all()
+            continue
+        if n <= 0:
+            assert (out[b] == 0).all() and (lse[b] == -float("inf")).all()
+            continue
+        at = torch.arange(max(0, n - c["window"]) if c["window"] else 0, n, device="cuda")
+        pg, off = c["table"][b].long()[at // page], at % page
+        for h in range(c["H"]):
+            kk, vv = k[pg, h, off].double(), v[pg, h, off].double()
+            if c["sc"][0] is not None:
+                kk, vv = kk * c["sc"][0][h].double(), vv * c["sc"][1][h].double()
+            rows = slice(h * G, (h + 1) * G)
+            q = c["q"][b, rows].double()
+            x = c["scale"] * (q @ kk.T)
+            size = c["scale"] * (q.abs() @ kk.abs().T).amax(1, keepdim=True)
+            dx = 2.0 ** -22 * size + 2.0 ** -22 * x.abs().amax(1, keepdim=True)
+            ref, ref_l = torch.softmax(x, 1) @ vv, torch.logsumexp(x, 1)
+            tol = (2 * dx + 2.0 ** -20) * vv.abs().amax()
+            if c["q"].dtype == torch.bfloat16:
+                tol = tol + 2.0 ** -12 * vv.abs().amax() + 2.0 ** -8 * ref.abs()
+            err = (out[b, rows] - ref).abs()
+            assert (err <= tol).all(), (b, h, n, float((err - tol).max()), float((err / tol).max()))
+            err = (lse[b, rows] - ref_l).abs()
+            tol = dx[:, 0] + 2.0 ** -20 * (1 + ref_l.abs())
+            assert (err <= tol).all(), (b, h, n, "lse", float((err / tol).max()))
+
+
+TYPES = [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.float8_e4m3fn),
+         (torch.float32, torch.float8_e4m3fn)]
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+@pytest.mark.parametrize("Hq,H,D,page", [
+    (1, 1, 64, 16), (8, 2, 128, 16), (16, 2, 256, 32), (12, 12, 80, 24), (7, 1, 96, 8), (32, 2, 64, 64), (24, 2, 192, 16),
+    (20, 1, 128, 1), (6, 2, 16, 5), (33, 1, 48, 128), (10, 1, 256, 100), (9, 1, 112, 7)])
+def test_attention_against_the_formula(m, q, cache, Hq, H, D, page):
+    """Head sizes and groups of every kind; lengths of none, one, and around
+    the ends of pages and tiles; short rows beside long ones."""
+    lens = [0, 1, page, page + 1, 2, 15, 16, 17, 63, 64, 65, 129, 700, -3, 1, 0, 1999]
+    c = _attend_case(m, lens, Hq, H, D, page, q, cache, seed=Hq * D + page)
+    _call(m, c)
+    _check(c)
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+@pytest.mark.parametrize("window", [1, 5, 16, 100, 1000, 5000])
+def test_attention_window(m, q, cache, window):
+    c = _attend_case(m, [0, 1, 4, 5, 6, 100, 101, 999, 1000, 1001, 3001], 8, 2, 128, 16, q, cache, window=window, seed=window)
+    _call(m, c)
+    _check(c)
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+@pytest.mark.parametrize("lens,Hq,H,D,page", [
+    ([20011], 8, 8, 128, 16), ([20011], 16, 1, 64, 64), ([9000, 1, 30001], 32, 2, 256, 24), ([1] * 300, 4, 2, 64, 16),
+    (list(range(0, 400, 3)), 6, 1, 80, 16), ([12007] * 5, 40, 2, 128, 256)])
+def test_attention_split_and_joined(m, q, cache, lens, Hq, H, D, page):
+    """Few long rows and many short ones: the split over the length."""
+    c = _attend_case(m, lens, Hq, H, D, page, q, cache, seed=len(lens))
+    _call(m, c)
+    _check(c)
+
+
+def test_attention_strides_and_a_cache_of_two_arrays(m):
+    for q in (torch.float32, torch.bfloat16):
+        c = _attend_case(m, [33, 0, 500], 8, 2, 64, 16, q, torch.bfloat16, split=True, pad=24, seed=5)
+        assert c["q"].stride(0) == 8 * 64 + 24
+        _call(m, c)
+        _check(c)
+        assert (c["out"][:, 8 * 64:] == 5.0).all()          # between the rows
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+def test_attention_of_large_scores(m, q, cache):
+    """Scores in the hundreds: the running maximum moves, weights underflow."""
+    c = _attend_case(m, [1, 40, 2000, 7001], 8, 2, 128, 16, q, cache, spread=1.5, seed=8)
+    c["scale"] = 4.0
+    _call(m, c)
+    _check(c)
+
+
+def test_attention_never_reads_through_a_bad_page_or_past_the_table(m):
+    for q, cache in TYPES:
+        c = _attend_case(m, [100, 3000, 64, 50, 17], 8, 2, 64, 16, q, cache, seed=2)
+        c["table"][1, 77] = c["desc"].n_pages                # a page that is not
+        c["table"][3, 0] = -1
+        c["lens"][2] = c["table"].shape[1] * 16 + 1          # longer than its row
+        c["seq"][2] = c["lens"][2]
+        _call(m, c)
+        _check(c, skip=(1, 2, 3))
+        c["window"] = 500                                    # the bad page of row 1 is out of the window
+        c["lens"][2] = 64
+        c["seq"][2] = 64
+        _call(m, c)
+        _check(c, skip=(3,))
+
+
+def test_attention_without_lse_and_of_no_rows(m):
+    c = _attend_case(m, [70, 3], 4, 2, 64, 16, torch.bfloat16, torch.bfloat16)
+    _call(m, c)
+    want, c["out"][:] = c["o"].clone(), 0
+    m.moe_paged_attention(c["desc"], c["q"], 2, 4, c["seq"], c["table"], c["table"].shape[1], c["scale"], c["o"], c["ws"])
+    assert torch.equal(c["o"], want)
+    m.moe_paged_attention(c["desc"], c["q"][:0], 0, 4, c["seq"], c["table"], c["table"].shape[1], c["scale"], c["o"][:0], c["ws"])
+
+
+def test_attention_gives_the_same_bits_again_and_on_another_stream(m):
+    for q, cache in TYPES:
+        c = _attend_case(m, [5000, 1, 0, 333, 12000], 16, 2, 128, 16, q, cache, seed=4)
+        _call(m, c)
+        want = c["o"].clone(), c["lse"].clone()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        for stream in (None, s, s):
+            c["out"].zero_()
+            c["ws"].fill_(17)
+            torch.cuda.synchronize()
+            _call(m, c, stream)
+            torch.cuda.synchronize()
+            assert torch.equal(c["o"], want[0]) and torch.equal(c["lse"], want[1])
+
+
+def test_attention_in_a_graph_follows_the_lengths(m):
+    """Captured once, replayed with other lengths and another table."""
+    c = _attend_case(m, [900, 17, 0], 8, 2, 64, 16, torch.bfloat16, torch.bfloat16, seed=6)
+    _call(m, c)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _call(m, c)
+    for lens in ([900, 17, 0], [33, 17, 0], [900, 1, 0]):
+        c["seq"].copy_(_ints(lens))
+        c["lens"] = lens
+        g.replay()
+        torch.cuda.synchronize()
+        _check(c)
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float8_e4m3fn])
+def test_cache_offsets_past_32_bits(m, cache):
+    """A cache of some 9 GB: pages whose numbers stand past 2^32 bytes and,
+    in 16 bits, past 2^32 numbers."""
+    H, page, D = 8, 64, 128
+    elt = 2 if cache == torch.bfloat16 else 1
+    P = (9 << 30) // (2 * H * page * D * elt)
+    kv = torch.empty((P, 2, H, page, D), dtype=cache, device="cuda")
+    ids = [P - 1, P // 2 + 1, 0, P - 7]
+    n = 3 * page + 9
+    slots = _ints([ids[t // page] * page + t % page for t in range(n)])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn((n, H, D), generator=g, device="cuda") for _ in range(2))
+    sc = (None, None) if elt == 2 else tuple(torch.full((H,), 0.01, device="cuda") for _ in range(2))
+    desc = _desc(m, kv, sc)
+    m.moe_kv_append(desc, k, v, slots, n)
+    for part, x, s in ((0, k, sc[0]), (1, v, sc[1])):
+        got = torch.stack([kv[ids[t // page], part, :, t % page].float() for t in range(n)])
+        x = x if s is None else (x / s[:, None]).clamp(-E4M3_MAX, E4M3_MAX)
+        assert torch.equal(got, x.to(cache).float())
+    table = _ints([ids])
+    q = torch.randn((1, 16, D), generator=g, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((1, 16), device="cuda")
+    c = dict(kv=kv, sc=sc, q=q, o=out, lse=lse, seq=_ints([n]), table=table, desc=desc, lens=[n], Hq=16, H=H, D=D, page=page, window=0,
+             split=False, scale=D ** -0.5,
+             ws=torch.empty(m.moe_paged_attention_workspace_bytes(desc, 1, 16), dtype=torch.uint8, device="cuda"))
+    _call(m, c)
+    _check(c)
+
+
+def test_plan_append_attend_together(m):
+    """Requests that grow from nothing, token by token and in prompts, with
+    pages that come back: the attention over the cache equals the one over
+    the keys as they were given."""
+    R, H, Hq, D, page, P, mb, cap = 5, 2, 6, 64, 8, 60, 20, 64
+    kv = torch.full((P, 2, H, page, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    desc = _desc(m, kv)
+    z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, ring = torch.full((R, mb), -1, dtype=torch.int32, device="cuda"), torch.arange(P, dtype=torch.int32, device="cuda")
+    seq, pool, first, slots, places, status = z(R), _ints([0, P]), z(R + 1), z(cap), z(cap), z(1)
+    keys = [[] for _ in range(R)]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rng = np.random.default_rng(3)
+    ws = torch.empty(m.moe_paged_attention_workspace_bytes(desc, R, Hq), dtype=torch.uint8, device="cuda")
+    for step in range(20):
+        new = [int(rng.integers(5, 13)) if not keys[r] else 1 for r in range(R)]
+        if step % 6 == 5:
+            new[step % R] = -1
+        seq_out, pool_out = z(R), z(2)
+        m.moe_kv_plan(seq, _ints(new), R, table, mb, page, ring, P, pool, seq_out, first, slots, places, cap, pool_out, status)
+        seq, pool = seq_out, pool_out
+        k, v = (torch.randn((cap, H, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+        m.moe_kv_append(desc, k, v, slots, cap)
+        i = 0
+        for r in range(R):
+            if new[r] < 0:
+                keys[r] = []
+            for _ in range(max(0, new[r])):
+                keys[r].append((k[i], v[i]))
+                i += 1
+        q = torch.randn((R, Hq, D), generator=g, device="cuda").bfloat16()
+        out, lse = torch.empty_like(q), torch.empty((R, Hq), device="cuda")
+        m.moe_paged_attention(desc, q, R, Hq, seq, table, mb, D ** -0.5, out, ws, lse=lse)
+        assert status.tolist() == [0] and seq.tolist() == [len(x) for x in keys]
+        for r in range(R):
+            if not keys[r]:
+                assert (out[r] == 0).all()
+                continue
+            kk = torch.stack([x[0] for x in keys[r]]).double().transpose(0, 1).repeat_interleave(Hq // H, 0)
+            vv = torch.stack([x[1] for x in keys[r]]).double().transpose(0, 1).repeat_interleave(Hq // H, 0)
+            x = torch.einsum("hd,hnd->hn", q[r].double(), kk) * D ** -0.5
+            ref = torch.einsum("hn,hnd->hd", torch.softmax(x, 1), vv)
+            # bf16's half unit, and 2^-12 + 2^-18 of the largest value for the weights and scores
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -12 + 2.0 ** -18) * vv.abs().amax()
+            assert ((out[r].double() - ref).abs() <= tol).all()

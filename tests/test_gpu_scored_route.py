@@ -1,0 +1,175 @@
+"""Routing by scores on the GPU (needs a GPU) against the rule in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    from int4_expert_gemv_gb300 import build
+    build.build()
+    from int4_expert_gemv_gb300 import moe
+    moe.lib()
+    return moe
+
+
+def _route(m, z, K, score="softmax", n_group=1, keep=1, best=1, renorm=True, factor=1.0, bias=None):
+    T, E = z.shape
+    rd = m.RouteDesc(E=E, K=K, score=m.MOE_SCORE_SIGMOID if score == "sigmoid" else m.MOE_SCORE_SOFTMAX, n_group=n_group,
+                     keep_group=keep, group_best=best, renorm=int(renorm), factor=factor,
+                     bias=None if bias is None else bias.data_ptr())
+    idx = torch.full((T, K), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((T, K), 9.0, device="cuda")
+    m.moe_scored_route(rd, z, T, idx, w)
+    return idx.cpu().numpy(), w.cpu().double().numpy()
+
+
+def _rule(z, K, score, n_group, keep, best, renorm, factor, bias):
+    """(idx, w, margin) of one token in 64 bits; margin: the smallest
+    difference between unequal neighbours of an order that was decided."""
+    E = len(z)
+    on = np.isfinite(z) | (z == np.inf)
+    s = np.zeros(E)
+    with np.errstate(over="ignore"):
+        if score == "sigmoid":
+            s[on] = 1.0 / (1.0 + np.exp(-z[on]))
+        elif on.any():
+            top = z[on].max()
+            e = np.where(z[on] == top, 1.0, np.exp(np.where(z[on] == top, 0.0, z[on]) - np.where(z[on] == top, 0.0, top)))
+            s[on] = e / e.sum()
+    c = np.where(on, s + (0.0 if bias is None else bias), -np.inf)
+    gs = E // n_group
+    margin = np.inf
+
+    def order(v, n):
+        nonlocal margin
+        o = np.argsort(-v, kind="stable")
+        for a, b in zip(o[:n], o[1:n + 1]):
+            if v[a] != v[b] and np.isfinite(v[b]):
+                margin = min(margin, v[a] - v[b])
+        return o[:n]
+
+    allowed = np.ones(E, bool)
+    if keep < n_group:
+        g = np.array([np.sort(c[j * gs:(j + 1) * gs])[::-1][:best].sum() for j in range(n_group)])
+        kept = order(g, keep)
+        allowed = np.isin(np.arange(E) // gs, kept)
+    cand = np.flatnonzero(allowed)
+    idx = cand[order(c[cand], K)]
+    w = s[idx]
+    if renorm:
+        w = w / w.sum() if w.sum() > 0 else np.zeros(K)
+    return idx, factor * w, margin
+
+
+def _check(m, z, K, **kw):
+    """Indices equal wherever the 64-bit rule's margin exceeds 2^-20 (scores
+    are at most 1, and fp32's exp, quotient and sums of up to 1024 terms keep
+    them within 2^-21 of exact); weights within 2^-18 relative (a score, the
+    sum of at most 16, a quotient) and the choices unequal otherwise."""
+    bias = kw.get("bias")
+    idx, w = _route(m, z, K, **kw)
+    zz = z.double().cpu().numpy()
+    b = None if bias is None else bias.double().cpu().numpy()
+    full = dict(score="softmax", n_group=1, keep=1, best=1, renorm=True, factor=1.0)
+    full.update({k: v for k, v in kw.items() if k != "bias"})
+    decided = 0
+    for t in range(len(zz)):
+        ref, rw, margin = _rule(zz[t], K, bias=b, **full)
+        assert len(set(idx[t])) == K and (0 <= idx[t]).all() and (idx[t] < zz.shape[1]).all()
+        if margin > 2.0 ** -20:
+            decided += 1
+            assert np.array_equal(idx[t], ref), (t, idx[t], ref, margin)
+            assert (np.abs(w[t] - rw) <= 2.0 ** -18 * np.abs(rw) + 1e-37).all(), (t, w[t], rw)
+    return decided
+
+
+SHAPES = [  # E, K, n_group, keep, best
+    (1, 1, 1, 1, 1), (16, 2, 1, 1, 1), (60, 4, 4, 2, 2), (64, 16, 8, 3, 2), (256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (512, 4, 1, 1, 1),
+    (160, 6, 8, 3, 1), (384, 8, 8, 8, 2), (1024, 16, 32, 5, 2), (1020, 3, 17, 2, 2), (96, 5, 3, 2, 2), (33, 7, 1, 1, 1), (32, 1, 32, 1, 1),
+    (1024, 16, 1, 1, 1)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,n_group,keep,best", SHAPES)
+def test_scored_route_against_the_rule(m, score, E, K, n_group, keep, best):
+    g = torch.Generator(device="cuda").manual_seed(E + K)
+    z = 1.5 * torch.randn((67, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    kw = dict(score=score, n_group=n_group, keep=keep, best=best)
+    n = 0
+    for x in (z, z.bfloat16()):
+        n += _check(m, x, K, **kw)
+        n += _check(m, x, K, bias=bias, renorm=False, factor=2.5, **kw)
+    assert n >= 200                                      # of 268: near-ties are rare
+
+
+def test_scored_route_ties_go_by_index(m):
+    z = torch.zeros((9, 64), device="cuda")
+    z[1, 40], z[2, ::2], z[3, 63], z[4] = 1.0, 2.0, -1.0, float("-inf")
+    z[5, 10:] = -0.0
+    for score in ("softmax", "sigmoid"):
+        for kw in (dict(), dict(n_group=8, keep=2, best=2), dict(n_group=4, keep=3, best=1)):
+            assert _check(m, z, 5, score=score, **kw) == 9
+    zero = torch.zeros(64, device="cuda")
+    zero[::3] = -0.0                                     # a bias of -0 changes nothing
+    idx, _ = _route(m, z[:1], 5, score="sigmoid", bias=zero)
+    assert idx[0].tolist() == [0, 1, 2, 3, 4]
+    idx, _ = _route(m, z[:1], 5, score="sigmoid", bias=zero - 0.5)   # choices of 0: +0 and -0 are one
+    assert idx[0].tolist() == [0, 1, 2, 3, 4]
+
+
+def test_scored_route_experts_that_are_off(m):
+    """-inf and NaN logits come after everything that is on and weigh 0; +inf
+    shares the mass; rows with nothing on get valid indices and zeros."""
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    z = torch.randn((8, 64), generator=g, device="cuda")
+    z[0, ::2] = -inf
+    z[1, 5:] = nan
+    z[2, :] = -inf
+    z[3, :] = nan
+    z[4, 7], z[4, 50] = inf, inf
+    z[5, :62] = torch.finfo(torch.float32).min
+    z[6, 1:] = -inf
+    z[7, 8:16], z[7, 20] = nan, inf
+    for score in ("softmax", "sigmoid"):
+        for kw in (dict(), dict(n_group=8, keep=3, best=2)):
+            idx, w = _route(m, z, 6, score=score, **kw)
+            assert np.isfinite(w).all() and (w >= 0).all()
+            full = dict(n_group=1, keep=1, best=1, renorm=True, factor=1.0, bias=None)
+            full.update(kw)
+            for t in range(8):
+                ref, rw, margin = _rule(z[t].double().cpu().numpy(), 6, score, **full)
+                assert len(set(idx[t])) == 6 and (0 <= idx[t]).all() and (idx[t] < 64).all()
+                if margin > 2.0 ** -20:
+                    assert np.array_equal(idx[t], ref), (score, kw, t, idx[t], ref)
+                    assert (np.abs(w[t] - rw) <= 2.0 ** -18 * rw + 1e-37).all()
+    bias = torch.full((64,), 10.0, device="cuda")        # a bias does not bring them back
+    idx, w = _route(m, z[6:7], 3, score="sigmoid", bias=bias)
+    assert idx[0].tolist() == [0, 1, 2] and w[0, 0] == 1.0 and (w[0, 1:] == 0).all()
+
+
+def test_scored_route_rows_of_a_wider_tensor(m):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for dt in (torch.float32, torch.bfloat16):
+        wide = torch.randn((50, 131), generator=g, device="cuda").to(dt)
+        z = wide[:, 3:63]                                # neither aligned nor contiguous
+        assert _check(m, z, 4, score="sigmoid", n_group=4, keep=2, best=2) > 40
+
+
+def test_scored_route_equals_topk_route_and_repeats(m):
+    """Softmax scores, no groups, renormalised: the framework's first route."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    z = torch.randn((300, 256), generator=g, device="cuda")
+    idx, w = _route(m, z, 4)
+    i2, w2 = torch.empty((300, 4), dtype=torch.int32, device="cuda"), torch.empty((300, 4), device="cuda")
+    m.moe_topk_route(z, 300, 256, 4, i2, w2)
+    near = (torch.sort(z, 1, descending=True).values[:, :5].diff(dim=1).abs() < 1e-5).any(1).cpu().numpy()
+    assert near.sum() < 5
+    assert np.array_equal(idx[~near], i2.cpu().numpy()[~near])
+    assert np.abs(w - w2.cpu().double().numpy())[~near].max() <= 2.0 ** -19
+    again = _route(m, z, 4)
+    assert np.array_equal(idx, again[0]) and np.array_equal(w, again[1])
