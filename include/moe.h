@@ -333,8 +333,8 @@ int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const v
  * multiples); lse fp32 [B][Hq], or NULL.  block_table [B][max_blocks].
  * A request of length <= 0 has out 0 and lse -inf.  Whatever stands in the
  * cache behind a request's length is without effect.  A page id outside
- * [0, n_pages), or a length above max_blocks * page, is never read through:
- * that request's out and lse are NaN.
+ * [0, n_pages), or a length above max_blocks * page (or 2^31 - 2^16), is never
+ * read through: that request's out and lse are NaN.
  * Scores, statistics and sums in fp32; products on the tensor cores from
  * numbers split so that an fp32 q and the softmax's weights keep fp32's
  * accuracy (with a BF16 result at least 2^-11 before it is rounded).

@@ -25,7 +25,8 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxe
 LIBS = {
     "libmoe.so": ["abi.cu", "pack.cu", "ffn.cu", "grouped.cu", "head_route.cu", "noalloc.cu",
                   "step.cu", "chain.cu", "lora_merge.cu", "gather.cu",
-                  "kv.cu", "attend.cu", "score_route.cu"],
+                  "kv.cu", "attend.cu", "attend_bf16_qf32.cu", "attend_bf16_qbf16.cu",
+                  "attend_e4m3_qf32.cu", "attend_e4m3_qbf16.cu", "score_route.cu"],
     "libmoe_synth.so": ["synth.cu"],
 }
 

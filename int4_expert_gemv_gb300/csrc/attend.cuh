@@ -1,0 +1,753 @@
+// attend.cuh -- attention of one new token per request over a paged key-value
+// cache: the kernel, templated over the head size, the cache's and the
+// query's type and the number of heads that share a key head.
+//
+// Mathematics.  A CTA walks part of one request's tokens for all (up to 16)
+// query heads of one key head, so every key and value is read once.  With
+// x_i = q . k_i, c = scale log2(e) (times the key scale) and a running
+// reference m >= c x_i, it keeps l = sum 2^(c x_i - m) and O = sum 2^(c x_i -
+// m) v_i; when m grows, l and O are multiplied by 2^(m_old - m_new).  Parts of
+// a row (warps of a CTA, then CTAs) join the same way: m = max m_j, l = sum
+// 2^(m_j - m) l_j, O likewise; out = O / l, lse = ln 2 (m + log2 l).
+//
+// What bounds it: the cache's bytes.  A key or value number is used by G
+// heads, 2 G flops for 2 bytes (bf16): far below the machine's balance, so the
+// design aims at bytes in flight and few instructions per byte, and the
+// products go to the tensor cores only to stay out of the way.  mma.sync with
+// its 16-row tile and register operands fits that: a tcgen05 tile has 64
+// rows or more of which G would be used, and its accumulator would have to
+// come out of tensor memory for every 64 tokens' softmax.
+//
+// Work split.  The unit is 64 tokens (16 for each of four warps) of one
+// (request, key head).  All units, in order of requests, heads and places, are
+// cut into one even run per CTA of a grid that is resident at once, whatever
+// the lengths: no row is too long and no batch too ragged.  A CTA thus holds
+// at most two partial rows, one cut at each end; it stores their (O, m, l)
+// and the join kernel adds them in order of the CTAs, so results do not
+// depend on timing.  Each CTA finds its run by summing the lengths itself.
+//
+// Pipeline.  Each warp streams its own 16-token tiles through a ring of NS
+// stages in shared memory with 16-byte asynchronous copies and waits only for
+// itself; there is no barrier until the row's end.  Rows are stored XOR-
+// swizzled so that the fragment loads below touch every bank once.
+//
+// Fragments.  In S = Q K^T the order of the k index is free as long as both
+// operands agree, so a lane's part of a key row is 16 consecutive bytes: k
+// steps of 16 numbers take 4 consecutive numbers of each of the row's four
+// lanes.  In O = P V the n index is free likewise: lane g's column of tile i
+// is dimension 8 g + i, and a lane reads 8 consecutive numbers of its four
+// token rows and pairs tokens with byte permutes.  P goes from accumulators to
+// operand registers without a shuffle.
+//
+// Accuracy.  bf16 and e4m3 keys and values are exact operands (e4m3 as fp16).
+// What is not exact is split into 16-bit parts that are summed in the fp32
+// accumulator: an fp32 q into three bf16 (24 bits) or two fp16 (22 bits, after
+// a power of two per row); the weights P into three bf16 or two fp16 with an
+// fp32 result, two bf16 (16 bits) or one fp16 (11 bits, 2^14 times the weight
+// so that small ones keep them) with a bf16 result, whose own rounding is
+// coarser.  With up to 8 heads the second part rides in the tile's
+// otherwise empty rows 8-15 and costs nothing.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace moe {
+
+constexpr int kAttWarps = 4;
+constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kAttTile = 16;                          // tokens of a warp's tile
+constexpr int kAttUnit = kAttTile * kAttWarps;        // tokens of a unit of work
+
+constexpr int kMaxLength = INT32_MAX - 65535;         // places past the last tile stay in 32 bits
+
+struct AttendParams {
+    const uint8_t *k, *v;
+    size_t page_stride;
+    const float *k_scale, *v_scale;
+    int n_pages, Hkv, D, B;
+    FastDiv page;
+    int G, tiles;                    // query heads of a key head; head tiles of them
+    const void *q;
+    size_t q_stride, out_stride;
+    int Hq;
+    const int32_t *seq, *table;
+    int max_blocks, window, ctas;
+    float scale;
+    void *out;
+    float *lse;
+    int4 *meta;                      // [ctas]: a row that starts in the CTA and goes on (pieces, request, head tile, first slot)
+    float2 *part_ml;                 // [2 ctas][rows]
+    float *part_o;                   // [2 ctas][rows][DP]
+};
+
+// ---------------------------------------------------------------- pieces
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ float exp2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two numbers as one 16-bit pair, and what the pair leaves of them.
+template <bool F16>
+__device__ __forceinline__ uint32_t pair_of(float &a, float &b) {
+    uint32_t w;
+    if (F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        const float2 f = __half22float2(h);
+        a -= f.x;
+        b -= f.y;
+        w = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        w = *reinterpret_cast<const uint32_t *>(&h);
+        a -= __uint_as_float(w << 16);
+        b -= __uint_as_float(w & 0xffff0000u);
+    }
+    return w;
+}
+
+// Two e4m3 (the low 16 bits) as an fp16 pair, exactly.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+    uint32_t r;
+    asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+    return r;
+}
+
+template <int DP, bool F8, bool QF32, bool FULL>
+struct AttendShape {
+    static constexpr int ELT = F8 ? 1 : 2;
+    static constexpr int CH = DP * ELT / 16;                  // 16-byte chunks of a row
+    static constexpr int NQ = QF32 ? (F8 ? 2 : 3) : 1;        // parts of q
+    static constexpr int NP = QF32 ? (F8 ? 2 : 3) : (F8 ? 1 : 2);   // parts of the weights
+    static constexpr int ROWS = FULL ? 16 : 8;                // query heads of a tile
+    static constexpr int NA = FULL ? NQ : (NQ + 1) / 2;       // operand tiles of q
+    static constexpr int NB = FULL ? NP : (NP + 1) / 2;       // of the weights
+    static constexpr int STEPS = DP / 16;
+    static constexpr int TILE_B = kAttTile * DP * ELT;        // bytes of a tile's keys (or values)
+    static constexpr int STAGE = 2 * TILE_B;
+    // Stages and CTAs per SM: 96 to 192 KB of stages per SM, two of three or
+    // more in flight.
+    static constexpr int NS = F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3) : (DP == 64 ? 6 : DP == 192 ? 4 : 3);
+    static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP <= 128 ? 2 : 1);
+    static constexpr int RING = NS * STAGE;                   // of one warp
+    static constexpr int Q_B = NA * STEPS * 512;
+    static constexpr int LDO = DP + 4;                        // floats of a row of O in the join of the warps
+    static constexpr int SMEM = kAttWarps * RING + Q_B;
+    static_assert(ROWS * LDO * 4 <= RING, "a warp's O fits its ring");
+};
+
+// Chunk c of row r of a tile: keys are read by 8 rows x 4 neighbouring
+// chunks, values by rows 2t x 8-byte or 16-byte chunks g.
+template <int CH>
+__device__ __forceinline__ uint32_t key_at(int r, int c) {
+    return CH >= 8 ? (uint32_t)(r * CH + (c ^ ((r & 1) << 2))) * 16 : (uint32_t)(r * CH + c) * 16;
+}
+template <int CH>
+__device__ __forceinline__ uint32_t value_at(int r, int c) {
+    if (CH >= 8) return (uint32_t)(r * CH + (c ^ (r & 6))) * 16;
+    const int pos = (r >> 1) | (r & 1) << 3;                  // rows of 64 bytes: even rows first
+    return (uint32_t)(pos * CH + (c ^ (pos & 2))) * 16;
+}
+
+__device__ __forceinline__ int units_of(int len, int window, int room) {
+    len = min(len, room);
+    if (len <= 0) return 0;
+    const int lo = window > 0 && len > window ? (len - window) & ~(kAttTile - 1) : 0;
+    return (len - lo + kAttUnit - 1) / kAttUnit;
+}
+
+template <bool QF32>
+__device__ __forceinline__ void store4(void *out, size_t i, float4 f) {
+    if (QF32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + i) = f;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
+__global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>::CTAS))
+    attend_kernel(const AttendParams p) {
+    using S = AttendShape<DP, F8, QF32, FULL>;
+    constexpr int CH = S::CH, NS = S::NS, ROWS = S::ROWS, R = FULL ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sm_sum[kAttWarps];
+    __shared__ int64_t sm_off;
+    __shared__ int sm_b, sm_bad;
+    __shared__ float sm_c[16];
+    __shared__ float2 sm_ml[kAttWarps][16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int cta = blockIdx.x, HT = p.Hkv * p.tiles;
+    const int room = (int)min((int64_t)p.max_blocks * p.page.d, (int64_t)kMaxLength);
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may take the SMs as they empty
+    uint8_t *ring = smem + warp * S::RING;
+    const uint32_t ring_a = smem_addr(ring);
+    uint4 *q_s = reinterpret_cast<uint4 *>(smem + kAttWarps * S::RING);
+
+    // where this CTA's run begins
+    const int run = (p.B + kAttThreads - 1) / kAttThreads;
+    const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; b++) sum += units_of(p.seq[b], p.window, room);
+    int64_t before = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+    }
+    if (lane == 31) sm_sum[warp] = before;
+    before -= sum;
+    for (int i = tid; i < S::Q_B / 16; i += kAttThreads) q_s[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    int64_t W = 0;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; w++) {
+        if (w == warp) before += W;
+        W += sm_sum[w];
+    }
+    W *= HT;
+    const int n_cta = (int)min((int64_t)p.ctas, W);
+    if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
+    int64_t u0 = 0, u1 = 0;
+    if (cta < n_cta) {
+        u0 = cta * W / n_cta;
+        u1 = (cta + 1) * W / n_cta;
+        if (u0 >= before * HT && u0 < (before + sum) * HT) {
+            int64_t at = before;
+            int b = b0;
+            for (;; b++) {
+                const int n = units_of(p.seq[b], p.window, room);
+                if (u0 < (at + n) * HT) break;
+                at += n;
+            }
+            sm_b = b;
+            sm_off = u0 - at * HT;
+        }
+    }
+    __syncthreads();
+
+    int b = cta < n_cta ? sm_b : 0;
+    int64_t off = cta < n_cta ? sm_off : 0;
+    bool first_seg = true;
+    for (int64_t u = u0; u < u1;) {
+        const int full_len = p.seq[b];
+        const int nb = units_of(full_len, p.window, room);
+        if (off >= (int64_t)nb * HT) {
+            off = 0;
+            b++;
+            continue;
+        }
+        const int ht = (int)(off / nb), blk = (int)(off - (int64_t)ht * nb);
+        const int n_unit = (int)min((int64_t)(nb - blk), u1 - u);
+        const int h = ht / p.tiles, head0 = h * p.G + (ht - h * p.tiles) * ROWS;
+        const int n_rows = min(ROWS, (h + 1) * p.G - head0);
+        const int len = min(full_len, room);
+        const int lo = p.window > 0 ? max(0, len - p.window) : 0;
+        const int tile0 = (lo & ~(kAttTile - 1)) + blk * kAttUnit;      // this segment's first token
+        const int stop = min(len, tile0 + n_unit * kAttUnit);
+        const int n_tile = (stop - tile0 + kAttTile - 1) / kAttTile;
+        const int mine = n_tile > warp ? (n_tile - warp + kAttWarps - 1) / kAttWarps : 0;
+        if (tid == 0) sm_bad = full_len > room;
+
+        // ---- q: split into parts, in the order of the operand's registers
+        const float c0 = p.scale * 1.44269504088896341f * (F8 && p.k_scale ? p.k_scale[h] : 1.0f);
+        for (int r = warp; r < ROWS; r += kAttWarps) {
+            constexpr int IT = (DP / 4 + 31) / 32;
+            float x[IT][4];
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < IT; i++) {
+                const int d = 4 * (lane + 32 * i);
+                x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
+                if (d < p.D && r < n_rows) {
+                    const size_t at = (size_t)b * p.q_stride + (size_t)(head0 + r) * p.D + d;
+                    if (QF32) {
+                        const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
+                        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+                    } else {
+                        const uint2 f = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + at);
+                        x[i][0] = __uint_as_float(f.x << 16), x[i][1] = __uint_as_float(f.x & 0xffff0000u);
+                        x[i][2] = __uint_as_float(f.y << 16), x[i][3] = __uint_as_float(f.y & 0xffff0000u);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) top = fmaxf(top, fabsf(x[i][j]));
+            }
+            float f = c0 < 0.0f ? -1.0f : 1.0f, c = fabsf(c0);
+            if (F8) {                     // fp16 parts: the row's largest number to 2^13 .. 2^14
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = max(27, (int)(__float_as_uint(top) >> 23));       // biased exponent
+                if (top > 0.0f && e < 255) {
+                    f *= __uint_as_float((uint32_t)(127 + 13 + 127 - e) << 23);
+                    c *= __uint_as_float((uint32_t)max(1, e - 13) << 23);
+                }
+            }
+            if (lane == 0) sm_c[r] = c;
+#pragma unroll
+            for (int i = 0; i < IT; i++) {
+                const int d = 4 * (lane + 32 * i);
+                if (d >= DP) break;
+                const int per = F8 ? 16 : 8;                       // numbers of a lane in a unit of the row
+                const int step = d / (4 * per) * (per / 4) + d % per / 4, tt = d / per % 4;
+#pragma unroll
+                for (int j = 0; j < 4; j++) x[i][j] *= f;
+#pragma unroll
+                for (int part = 0; part < S::NQ; part++) {
+                    const int na = FULL ? part : part / 2, up = FULL ? r >> 3 : part & 1;
+                    uint32_t *w = reinterpret_cast<uint32_t *>(q_s + (na * S::STEPS + step) * 32 + (r & 7) * 4 + tt);
+                    w[up] = pair_of<F8>(x[i][0], x[i][1]);
+                    w[2 + up] = pair_of<F8>(x[i][2], x[i][3]);
+                }
+            }
+        }
+        __syncthreads();
+        float c[R], m[R], l[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            c[r] = sm_c[g + 8 * r];
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+        }
+        float o[DP / 8][4];
+#pragma unroll
+        for (int i = 0; i < DP / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+
+        // ---- the warp's tiles
+        const int row_b = p.D * S::ELT;                            // bytes of a stored row
+        const size_t head_b = (size_t)h * p.page.d * row_b;
+        const int32_t *tab = p.table + (size_t)b * p.max_blocks;
+        int ids = 0;                    // ALIGNED: the pages of 32 tiles; else of the next tile's rows
+        bool bad = false;
+        auto page_of = [&](int tok) { return tok < stop ? tab[p.page.div(tok)] : -1; };
+        auto fetch_ids = [&](int i) {   // before tile i is issued
+            if (ALIGNED) {
+                if ((i & 31) == 0) ids = page_of(tile0 + (warp + kAttWarps * (i + lane)) * kAttTile);
+            } else {
+                ids = page_of(tile0 + (warp + kAttWarps * i) * kAttTile + (lane & 15));
+            }
+        };
+        auto issue = [&](int i) {
+            if (i < mine) {
+                const int tok0 = tile0 + (warp + kAttWarps * i) * kAttTile;
+                const uint32_t dst = ring_a + (i % NS) * S::STAGE;
+                size_t base = 0;
+                bool ok0 = false;
+                if (ALIGNED) {
+                    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+                    ok0 = (unsigned)id < (unsigned)p.n_pages;
+                    const int in = tok0 - p.page.div(tok0) * p.page.d;
+                    base = (ok0 ? (size_t)id : 0) * p.page_stride + head_b + (size_t)in * row_b;
+                    bad |= !ok0;
+                    fetch_ids(i + 1);
+                } else {
+                    const int tok = tok0 + (lane & 15);
+                    ok0 = (unsigned)ids < (unsigned)p.n_pages;
+                    bad |= !ok0 && tok >= lo && tok < stop;
+                    const int in = tok - p.page.div(tok) * p.page.d;
+                    base = (ok0 ? (size_t)ids : 0) * p.page_stride + head_b + (size_t)in * row_b;
+                    fetch_ids(i + 1);
+                }
+#pragma unroll
+                for (int n = 0; n < CH * kAttTile / 32; n++) {
+                    const int e = n * 32 + lane, r = e / CH, ch = e - r * CH;
+                    size_t at = base + (size_t)(r * row_b);
+                    bool ok = ok0;
+                    if (!ALIGNED) {
+                        at = __shfl_sync(0xffffffffu, (unsigned long long)base, r);
+                        ok = __shfl_sync(0xffffffffu, (int)ok0, r);
+                    }
+                    at += ch * 16;
+                    const int tok = tok0 + r;
+                    ok = ok && tok >= lo && tok < stop && ch * 16 < row_b;
+                    at = ok ? at : 0;
+                    copy16(dst + key_at<CH>(r, ch), p.k + at, ok);
+                    copy16(dst + S::TILE_B + value_at<CH>(r, ch), p.v + at, ok);
+                }
+            }
+            copy_commit();
+        };
+        fetch_ids(0);
+#pragma unroll
+        for (int i = 0; i < NS - 1; i++) issue(i);
+        for (int i = 0; i < mine; i++) {
+            __syncwarp();
+            issue(i + NS - 1);
+            copy_wait<NS - 1>();
+            __syncwarp();
+            const uint32_t ks = ring_a + (i % NS) * S::STAGE, vs = ks + S::TILE_B;
+            const int tok0 = tile0 + (warp + kAttWarps * i) * kAttTile;
+
+            float s[2][4] = {};
+#pragma unroll
+            for (int un = 0; un < CH / 4; un++) {
+                const uint4 k0 = lds16(ks + key_at<CH>(g, 4 * un + t));
+                const uint4 k1 = lds16(ks + key_at<CH>(g + 8, 4 * un + t));
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int j = 0; j < (F8 ? 4 : 2); j++) {
+                    const int step = un * (F8 ? 4 : 2) + j;
+                    uint32_t x0, x1, y0, y1;
+                    if (F8) {
+                        x0 = e4m3_pair(w0[j]), x1 = e4m3_pair(w0[j] >> 16);
+                        y0 = e4m3_pair(w1[j]), y1 = e4m3_pair(w1[j] >> 16);
+                    } else {
+                        x0 = w0[2 * j], x1 = w0[2 * j + 1];
+                        y0 = w1[2 * j], y1 = w1[2 * j + 1];
+                    }
+#pragma unroll
+                    for (int na = 0; na < S::NA; na++) {
+                        const uint4 a = q_s[(na * S::STEPS + step) * 32 + lane];
+                        mma<F8>(s[0], a.x, a.y, a.z, a.w, x0, x1);
+                        mma<F8>(s[1], a.x, a.y, a.z, a.w, y0, y1);
+                    }
+                }
+            }
+            // x[r][4]: tokens 2t, 2t+1, 2t+8, 2t+9 of head g (and g + 8)
+            float x[R][4];
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    if (FULL) {
+                        x[0][2 * n + j] = s[n][j];
+                        x[R - 1][2 * n + j] = s[n][2 + j];
+                    } else {
+                        x[0][2 * n + j] = S::NQ > 1 ? s[n][j] + s[n][2 + j] : s[n][j];
+                    }
+                }
+            if (tok0 < lo || tok0 + kAttTile > stop) {
+#pragma unroll
+                for (int n = 0; n < 4; n++) {
+                    const int tok = tok0 + (n >> 1) * 8 + 2 * t + (n & 1);
+                    if (tok < lo || tok >= stop) {
+#pragma unroll
+                        for (int r = 0; r < R; r++) x[r][n] = -INFINITY;
+                    }
+                }
+            }
+            float f[R];
+            bool moved = false;
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float mn = fmaxf(m[r], top * c[r] - (F8 ? 14.0f : 0.0f));
+                f[r] = 1.0f;
+                if (mn > m[r]) {
+                    f[r] = exp2_f(m[r] - mn);
+                    m[r] = mn;
+                    moved = true;
+                }
+                const float ref = mn == -INFINITY ? 0.0f : mn;
+                float add = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 4; n++) {
+                    x[r][n] = exp2_f(fmaf(x[r][n], c[r], -ref));
+                    add += x[r][n];
+                }
+                l[r] = fmaf(l[r], f[r], add);
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int i2 = 0; i2 < DP / 8; i2++) {
+                    o[i2][0] *= f[0];
+                    o[i2][1] *= f[0];
+                    o[i2][2] *= f[R - 1];
+                    o[i2][3] *= f[R - 1];
+                }
+            }
+            // the weights as operand tiles
+            uint32_t a[S::NB][4];
+#pragma unroll
+            for (int nb2 = 0; nb2 < S::NB; nb2++) a[nb2][1] = a[nb2][3] = 0u;
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int part = 0; part < S::NP; part++) {
+                    const int to = FULL ? part : part / 2, up = FULL ? r : part & 1;
+                    a[to][up] = pair_of<F8>(x[r][0], x[r][1]);
+                    a[to][2 + up] = pair_of<F8>(x[r][2], x[r][3]);
+                }
+#pragma unroll
+            for (int un = 0; un < DP / 64; un++) {
+                uint32_t v[2][8];                   // operand registers of the 8 tiles of 8 dimensions
+                if (F8) {
+                    const int ch = 4 * un + (g >> 1), in = (g & 1) * 8;
+                    uint2 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        w[j] = lds8(vs + value_at<CH>(2 * t + (j & 1) + (j >> 1) * 8, ch) + in);
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                        for (int q4 = 0; q4 < 2; q4++) {
+                            const uint32_t e = q4 ? w[2 * hf].y : w[2 * hf].x;
+                            const uint32_t d = q4 ? w[2 * hf + 1].y : w[2 * hf + 1].x;
+                            const uint32_t lo2 = __byte_perm(e, d, 0x5140), hi2 = __byte_perm(e, d, 0x7362);
+                            v[hf][4 * q4] = e4m3_pair(lo2);
+                            v[hf][4 * q4 + 1] = e4m3_pair(lo2 >> 16);
+                            v[hf][4 * q4 + 2] = e4m3_pair(hi2);
+                            v[hf][4 * q4 + 3] = e4m3_pair(hi2 >> 16);
+                        }
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        const uint4 e = lds16(vs + value_at<CH>(2 * t + 8 * hf, 8 * un + g));
+                        const uint4 d = lds16(vs + value_at<CH>(2 * t + 1 + 8 * hf, 8 * un + g));
+                        const uint32_t ew[4] = {e.x, e.y, e.z, e.w}, dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            v[hf][2 * j] = __byte_perm(ew[j], dw[j], 0x5410);
+                            v[hf][2 * j + 1] = __byte_perm(ew[j], dw[j], 0x7632);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+#pragma unroll
+                    for (int nb2 = 0; nb2 < S::NB; nb2++)
+                        mma<F8>(o[un * 8 + j], a[nb2][0], a[nb2][1], a[nb2][2], a[nb2][3], v[0][j], v[1][j]);
+            }
+        }
+        copy_wait<0>();
+        __syncwarp();
+
+        // ---- the warps' parts of the row
+        if (bad) sm_bad = 1;
+        float *o_s = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (t == 0) sm_ml[warp][g + 8 * r] = make_float2(m[r], l[r]);
+#pragma unroll
+            for (int un = 0; un < DP / 64; un++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                    for (int q4 = 0; q4 < 2; q4++) {
+                        float4 w;
+                        float *wf = &w.x;
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float *e = o[un * 8 + 4 * q4 + j];
+                            wf[j] = FULL ? e[2 * r + hf] : e[hf] + e[2 + hf];
+                        }
+                        *reinterpret_cast<float4 *>(o_s + (g + 8 * r) * S::LDO + un * 64 + 16 * t + 8 * hf + 4 * q4) = w;
+                    }
+        }
+        __syncthreads();
+        const bool whole = n_unit == nb;
+        const float v_scale = F8 && p.v_scale ? p.v_scale[h] : 1.0f;
+        const int slot = 2 * cta + (first_seg ? 0 : 1);
+        for (int i = tid; i < n_rows * (DP / 4); i += kAttThreads) {
+            const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttWarps; w++) M = fmaxf(M, sm_ml[w][r].x);
+            const float ref = M == -INFINITY ? 0.0f : M;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kAttWarps; w++) {
+                const float2 ml = sm_ml[w][r];
+                const float fw = exp2_f(ml.x - ref);
+                const float4 e = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem + w * S::RING) + r * S::LDO + d);
+                L = fmaf(fw, ml.y, L);
+                acc.x = fmaf(fw, e.x, acc.x);
+                acc.y = fmaf(fw, e.y, acc.y);
+                acc.z = fmaf(fw, e.z, acc.z);
+                acc.w = fmaf(fw, e.w, acc.w);
+            }
+            if (sm_bad) L = NAN;
+            if (whole) {
+                const float inv = v_scale / L;
+                if (d < p.D)
+                    store4<QF32>(p.out, (size_t)b * p.out_stride + (size_t)(head0 + r) * p.D + d,
+                                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                if (d == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + r] = 0.69314718055994531f * (M + log2f(L));
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + ((size_t)slot * ROWS + r) * DP + d) = acc;
+                if (d == 0) p.part_ml[(size_t)slot * ROWS + r] = make_float2(M, L);
+            }
+        }
+        if (tid == 0 && blk == 0 && n_unit < nb) {
+            const int64_t last = u + nb - 1;                       // the row's last unit, and its CTA
+            const int c1 = (int)(((last + 1) * n_cta - 1) / W);
+            p.meta[cta] = make_int4(c1 - cta + 1, b, ht, slot);
+        }
+        __syncthreads();
+        first_seg = false;
+        u += n_unit;
+        off += n_unit;
+    }
+
+    // rows with nothing to see
+    for (int e = cta; e < p.B; e += gridDim.x) {
+        if (units_of(p.seq[e], p.window, room) > 0) continue;
+        for (int i = tid; i < p.Hq * p.D / 4; i += kAttThreads)
+            store4<QF32>(p.out, (size_t)e * p.out_stride + 4 * (size_t)i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        if (p.lse)
+            for (int i = tid; i < p.Hq; i += kAttThreads) p.lse[(size_t)e * p.Hq + i] = -INFINITY;
+    }
+}
+
+// Joins a row's parts, one CTA per (CTA of the row's first part, head): the
+// warps take every eighth part, their lanes four dimensions each.
+template <bool QF32>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int dp, int rows) {
+    __shared__ float4 acc_s[8][64];
+    __shared__ float red[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 meta = p.meta[blockIdx.x];
+    const int n = meta.x, b = meta.y, r = blockIdx.y;
+    if (n == 0) return;
+    const int h = meta.z / p.tiles, head0 = h * p.G + (meta.z - h * p.tiles) * rows;
+    if (head0 + r >= (h + 1) * p.G) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto slot = [&](int j) { return j == 0 ? (size_t)meta.w : 2 * ((size_t)blockIdx.x + j); };
+    float M = -INFINITY;
+    for (int j = tid; j < n; j += 256) M = fmaxf(M, p.part_ml[slot(j) * rows + r].x);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    for (int w = 0; w < 8; w++) M = fmaxf(M, red[w]);
+    __syncthreads();
+    const float ref = M == -INFINITY ? 0.0f : M;
+    const int q = dp / 4;                            // float4s of a row: 16 .. 64
+    float L = 0.0f;
+    float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+#pragma unroll 4
+    for (int j = warp; j < n; j += 8) {
+        const size_t s = slot(j) * rows + r;
+        const float2 ml = p.part_ml[s];
+        const float f = exp2_f(ml.x - ref);
+        L = fmaf(f, ml.y, L);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (lane + 32 * i < q) {
+                const float4 e = *reinterpret_cast<const float4 *>(p.part_o + s * dp + 4 * (lane + 32 * i));
+                acc[i].x = fmaf(f, e.x, acc[i].x);
+                acc[i].y = fmaf(f, e.y, acc[i].y);
+                acc[i].z = fmaf(f, e.z, acc[i].z);
+                acc[i].w = fmaf(f, e.w, acc[i].w);
+            }
+        }
+    }
+    acc_s[warp][lane] = acc[0];
+    acc_s[warp][lane + 32] = acc[1];
+    if (lane == 0) red[warp] = L;
+    __syncthreads();
+    if (tid < q && 4 * tid < p.D) {
+        float4 a = make_float4(0, 0, 0, 0);
+        L = 0.0f;
+        for (int w = 0; w < 8; w++) {
+            const float4 e = acc_s[w][tid];
+            a.x += e.x, a.y += e.y, a.z += e.z, a.w += e.w;
+            L += red[w];
+        }
+        const float inv = (p.v_scale ? p.v_scale[h] : 1.0f) / L;
+        store4<QF32>(p.out, (size_t)b * p.out_stride + (size_t)(head0 + r) * p.D + 4 * tid,
+                     make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        if (tid == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + r] = 0.69314718055994531f * (M + log2f(L));
+    }
+}
+
+// ---------------------------------------------------------------- launch
+template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
+int launch_attend_kernel(const AttendParams &p, cudaStream_t st) {
+    using S = AttendShape<DP, F8, QF32, FULL>;
+    auto kernel = attend_kernel<DP, F8, QF32, FULL, ALIGNED>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e == cudaSuccess) {
+        kernel<<<p.ctas, kAttThreads, S::SMEM, st>>>(p);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_kernel: %s", cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)min(S::ROWS, p.G));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32>, p, DP, (int)S::ROWS);
+    if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_join_kernel: %s", cudaGetErrorString(e));
+    return MOE_OK;
+}
+
+// CTAs per SM, padded head size and tile rows of a shape; the workspace goes by them.
+struct AttendPlan {
+    int dp, rows, ctas_per_sm;
+};
+inline AttendPlan attend_plan(int D, bool f8, int G) {
+    AttendPlan a;
+    a.dp = D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 && !f8 ? 192 : 256;
+    a.rows = G > 8 ? 16 : 8;
+    a.ctas_per_sm = f8 ? (a.dp == 256 ? 2 : 3) : (a.dp <= 128 ? 2 : 1);
+    return a;
+}
+
+template <bool F8, bool QF32, int DP>
+int launch_attend_dp(const AttendParams &p, cudaStream_t st) {
+    const bool full = p.G > 8, aligned = p.page.d % kAttTile == 0;
+    if (full) return aligned ? launch_attend_kernel<DP, F8, QF32, true, true>(p, st)
+                             : launch_attend_kernel<DP, F8, QF32, true, false>(p, st);
+    return aligned ? launch_attend_kernel<DP, F8, QF32, false, true>(p, st)
+                   : launch_attend_kernel<DP, F8, QF32, false, false>(p, st);
+}
+
+int launch_attend_bf16_qf32(const AttendParams &p, int dp, cudaStream_t st);
+int launch_attend_bf16_qbf16(const AttendParams &p, int dp, cudaStream_t st);
+int launch_attend_e4m3_qf32(const AttendParams &p, int dp, cudaStream_t st);
+int launch_attend_e4m3_qbf16(const AttendParams &p, int dp, cudaStream_t st);
+
+}  // namespace moe
