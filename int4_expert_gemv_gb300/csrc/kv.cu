@@ -162,20 +162,46 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         p.ring[(int)(((int64_t)head + n_free + j) % p.n_pages)] =
             p.table[(size_t)r * p.max_blocks + j - s_gone[r]];
     }
-    // slots and places
-    for (int i = me; i < p.cap; i += step) {
-        int slot = -1, place = 0;
-        if (i < n_new) {
-            const int r = owner(s_new, R, i);
-            const int len = p.seq[r];
-            place = len + i - s_new[r];
-            const int b = p.page.div(place), have = p.page.ceil(len);
-            const int id = b < have ? p.table[(size_t)r * p.max_blocks + b]
-                                    : p.ring[wrap((int64_t)head + s_need[r] + b - have, p.n_pages)];
-            if ((unsigned)id < (unsigned)p.n_pages) slot = id * page + place - b * page;
+    // slots and places, four neighbours a thread: one search for the first, and
+    // a new length, block or page only where it changes
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.places)) & 15) == 0;
+    for (int64_t i0 = 4 * (int64_t)me; i0 < p.cap; i0 += 4 * (int64_t)step) {
+        int slot[4] = {-1, -1, -1, -1}, place[4] = {0, 0, 0, 0};
+        if (i0 < n_new) {
+            int r = owner(s_new, R, (int)i0), next = r + 1 < R ? s_new[r + 1] : n_new;
+            int len = p.seq[r], have = p.page.ceil(len), blk = -1, id = -1;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int i = (int)i0 + j;
+                if (i >= n_new) break;
+                if (i >= next) {
+                    do {
+                        r++;
+                        next = r + 1 < R ? s_new[r + 1] : n_new;
+                    } while (i >= next);
+                    len = p.seq[r];
+                    have = p.page.ceil(len);
+                    blk = -1;
+                }
+                place[j] = len + i - s_new[r];
+                const int b = p.page.div(place[j]);
+                if (b != blk) {
+                    blk = b;
+                    id = b < have ? p.table[(size_t)r * p.max_blocks + b]
+                                  : p.ring[wrap((int64_t)head + s_need[r] + b - have, p.n_pages)];
+                }
+                if ((unsigned)id < (unsigned)p.n_pages) slot[j] = id * page + place[j] - b * page;
+            }
         }
-        p.slots[i] = slot;
-        p.places[i] = place;
+        if (vec && i0 + 4 <= p.cap) {
+            *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(p.places + i0) = make_int4(place[0], place[1], place[2], place[3]);
+        } else {
+            for (int j = 0; j < 4 && i0 + j < p.cap; j++) {
+                p.slots[i0 + j] = slot[j];
+                p.places[i0 + j] = place[j];
+            }
+        }
     }
 }
 

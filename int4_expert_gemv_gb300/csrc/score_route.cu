@@ -2,13 +2,27 @@
 // logits, a balance bias that moves only the choice, groups of experts of
 // which a few stay, the K best of those and their renormalised weights.
 //
-// One warp per token.  The group count is rounded up to a power of two that
-// divides the warp, so a group is 32 / that many neighbouring lanes, each
-// with NV consecutive experts of it: a group's best two come from log2 steps
-// of shuffles for all groups at once, and equal choices resolve to the lowest
-// lane, then the lowest register -- the lowest index.  Choices are compared as
-// 32-bit keys that order like the numbers, so a round of the top-K is one
-// warp-wide integer maximum and a ballot.
+// Layout.  LT lanes (8 or 32) share a token.  A group's experts stand in
+// blocks of 8 (the last one short), block s of the token with lane s mod LT:
+// one lane reads 32 or 16 bytes of a row, its neighbours the next ones.  A
+// lane keeps each of its blocks' largest choice in a register and all
+// choices in shared memory.  A round of the top-K is then a maximum over a
+// lane's blocks and over LT lanes; only the lane that had it looks into
+// that one block again.  With 8 lanes a warp does so for four tokens at
+// once, which is what the rounds cost most of; with 32 a token has the
+// shorter chain.  Choices are floats: what is off is -FLT_MAX (all other
+// choices are kept at or above it), what is taken or dropped -inf.
+//
+// Bound.  The logits are read once (4 E bytes a token, 10.5 us for 65521
+// tokens of 256 at the copy rate) and each costs an exponential and a
+// reciprocal for its sigmoid: 16 of those a clock and SM make 7 us there.
+// Measured 34.8 us with bias and 4 of 8 groups, K = 8: instruction issue
+// bounds it (68 % of the issue slots); a round costs 1.5 us, the groups 4.5,
+// the bias 2, and the rest 17.6.  A warp per token with a warp-wide integer
+// maximum per round took 68 us.
+#include <cfloat>
+#include <type_traits>
+
 #include "internal.h"
 
 namespace moe {
@@ -18,24 +32,16 @@ namespace {
 struct RouteParams {
     const void *z;
     size_t stride;
-    int T, E, K, n_group, gs, lanes, keep, best, renorm;   // gs: experts of a group, lanes: of a group
+    int T, E, K, n_group, gs, nsub, keep, best, renorm;   // gs: experts of a group, nsub: blocks of a token
+    FastDiv spg;                                          // blocks of a group
+    int vec;                                              // whole blocks, 16-byte aligned
     float factor;
     const float *bias;
     int32_t *idx;
     float *w;
 };
 
-constexpr uint32_t kOut = 0u;                 // no expert, or one of a dropped group
-
-// Orders as the numbers do (NaN excluded); -0 is made +0 first.
-__device__ __forceinline__ uint32_t order_key(float c) {
-    const uint32_t u = __float_as_uint(c + 0.0f);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
+constexpr int kRouteThreads = 128;
 
 template <typename X>
 __device__ __forceinline__ float logit(const void *row, int e);
@@ -48,126 +54,351 @@ __device__ __forceinline__ float logit<__nv_bfloat16>(const void *row, int e) {
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]);
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
+template <typename X>
+__device__ __forceinline__ void logits8(const void *row, int e, float *f);
+template <>
+__device__ __forceinline__ void logits8<float>(const void *row, int e, float *f) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void logits8<__nv_bfloat16>(const void *row, int e, float *f) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(row) + e));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
 
-// exp(z - m) with +inf logits sharing the mass
+// The choice goes by quick scores (2^-21 of exact), equal for equal logits;
+// the weights of the chosen by exact exponentials and quotients.
+__device__ __forceinline__ float quick_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float quick_sigmoid(float z) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + quick_exp2(z * -1.44269504088896341f)));
+    return y;
+}
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
+// exp(z - m), +inf logits sharing the mass.
 __device__ __forceinline__ float soft_f(float z, float m) { return z == m ? 1.0f : expf(z - m); }
 
-template <typename X, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(256) scored_route_kernel(const RouteParams p) {
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (t >= p.T) return;                     // whole warps
+template <int LT>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = LT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int LT>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Shared memory of a token: its choices (the first, then the second float4 of
+// every block, so that neighbouring lanes meet no bank twice), the blocks'
+// best two, the places of the chosen.
+__host__ __device__ constexpr int route_token_floats(int LT, int SUB) { return LT * SUB * 10 + 16; }
+
+template <typename X, int LT, int SUB, bool SIGMOID, bool VEC>
+__global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const RouteParams p) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int TOK = kRouteThreads / LT, NB = LT * SUB;
+    const int lane = threadIdx.x & 31, sub = threadIdx.x / LT, l = threadIdx.x % LT;
+    const int tt = blockIdx.x * TOK + sub;
+    const bool live = tt < p.T;
+    const int t = live ? tt : p.T - 1;             // the last warp's idle lanes repeat a token
+    float *c_s = smem + sub * route_token_floats(LT, SUB);
+    float4 *c4 = reinterpret_cast<float4 *>(c_s);
+    float2 *best_s = reinterpret_cast<float2 *>(c_s + NB * 8);
+    int *pick_s = reinterpret_cast<int *>(c_s + NB * 10);
     const X *row = static_cast<const X *>(p.z) + (size_t)t * p.stride;
-    const int group = lane / p.lanes, first = (lane - group * p.lanes) * NV;
-    const int base = group * p.gs + first;
-    const int n = group < p.n_group ? min(NV, max(0, p.gs - first)) : 0;   // this lane's experts
+    const bool groups = p.keep < p.n_group;
 
-    float s[NV];
+    // first expert of block s
+    auto expert0 = [&](int s) {
+        const int grp = p.spg.div(s);
+        return grp * p.gs + (s - grp * p.spg.d) * 8;
+    };
+    // how many of block s's places have an expert (s < nsub)
+    auto count = [&](int s) { return VEC ? 8 : p.gs - (s - p.spg.div(s) * p.spg.d) * 8; };
+    // block s's eight numbers of a row of E; -inf where there is no expert
+    auto read8 = [&](auto *x, int s, float *f) {
+        using Y = typename std::remove_const<typename std::remove_pointer<decltype(x)>::type>::type;
+        if (VEC) {
+            logits8<Y>(x, expert0(s), f);
+        } else {
+            const int e0 = expert0(s), n = count(s);
 #pragma unroll
-    for (int i = 0; i < NV; i++) s[i] = i < n ? logit<X>(row, base + i) : -INFINITY;
-    float m = -INFINITY, inv = 0.0f;
-    if (!SIGMOID) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) m = fmaxf(m, s[i]);          // NaN is passed over
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const bool on = s[i] > -INFINITY;                    // neither -inf nor NaN
-            const float e = on ? soft_f(s[i], m) : 0.0f;
-            sum += e;
-            s[i] = on ? e : -INFINITY;
+            for (int i = 0; i < 8; i++) f[i] = i < n ? logit<Y>(x, e0 + i) : -INFINITY;
         }
-        sum = warp_sum(sum, 32);
-        inv = sum;
-    }
-    uint32_t key[NV];
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const bool on = s[i] > -INFINITY;
-        float c = -INFINITY;
-        if (on) {
-            c = SIGMOID ? sigmoid_f(s[i]) : __fdiv_rn(s[i], inv);
-            if (p.bias) c += __ldg(p.bias + base + i);
-            if (c != c) c = -INFINITY;
-        }
-        key[i] = i < n ? order_key(c) : kOut;
-    }
+    };
+    auto put8 = [&](int s, const float *f) {
+        c4[s] = make_float4(f[0], f[1], f[2], f[3]);
+        c4[NB + s] = make_float4(f[4], f[5], f[6], f[7]);
+    };
+    auto get8 = [&](int s, float *f) {
+        const float4 a = c4[s], b = c4[NB + s];
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    };
 
-    if (p.keep < p.n_group) {
-        uint32_t b1 = kOut, b2 = kOut;
+    float m = -INFINITY, total = 1.0f;
+    if (!SIGMOID) {                                 // the exponentials, and their sum
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            b2 = max(b2, min(b1, key[i]));
-            b1 = max(b1, key[i]);
-        }
-        for (int o = p.lanes >> 1; o > 0; o >>= 1) {
-            const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b1, o);
-            const uint32_t o2 = __shfl_xor_sync(0xffffffffu, b2, o);
-            b2 = max(max(b2, o2), min(b1, o1));
-            b1 = max(b1, o1);
-        }
-        float g = p.best == 1 ? key_value(b1) : key_value(b1) + key_value(b2);
-        if (g != g) g = -INFINITY;
-        const uint32_t mine = order_key(g);
-        int rank = 0;
-        for (int j = 0; j < p.n_group; j++) {
-            const uint32_t other = __shfl_sync(0xffffffffu, mine, j * p.lanes);
-            rank += other > mine || (other == mine && j < group);
-        }
-        if (rank >= p.keep) {
+        for (int j = 0; j < SUB; j++) {
+            const int s = l + LT * j;
+            if (s < p.nsub) {
+                float f[8];
+                read8(row, s, f);
 #pragma unroll
-            for (int i = 0; i < NV; i++) key[i] = kOut;
-        }
-    }
-
-    int chosen = 0;                           // lane k: the k-th choice
-    for (int k = 0; k < p.K; k++) {
-        uint32_t b = key[0];
-        int bi = 0;
-#pragma unroll
-        for (int i = 1; i < NV; i++)
-            if (key[i] > b) {
-                b = key[i];
-                bi = i;
+                for (int i = 0; i < 8; i++) m = fmaxf(m, f[i]);        // passes NaN over
+                put8(s, f);
             }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, b);
-        const int src = __ffs(__ballot_sync(0xffffffffu, b == top)) - 1;
-        const int e = __shfl_sync(0xffffffffu, base + bi, src);
-        if (lane == k) chosen = e;
-        if (lane == src) {
+        }
+        m = lanes_max<LT>(m);
+        const bool share = __any_sync(0xffffffffu, m == INFINITY);     // +inf logits share the mass
+        const float ref = m == INFINITY || m == -INFINITY ? 0.0f : m * 1.44269504088896341f;
+        total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                if (i == bi) key[i] = kOut;
+        for (int j = 0; j < SUB; j++) {
+            const int s = l + LT * j;
+            if (s < p.nsub) {
+                float f[8];
+                get8(s, f);
+                if (share && m == INFINITY) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (f[i] > -INFINITY) f[i] = f[i] == INFINITY ? 0.0f : -FLT_MAX;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float e = quick_exp2(fmaf(f[i], 1.44269504088896341f, -ref));
+                    f[i] = f[i] > -INFINITY ? e : -FLT_MAX;            // off: -inf and NaN
+                    total += fmaxf(f[i], 0.0f);
+                }
+                put8(s, f);
+            }
+        }
+        total = lanes_sum<LT>(total);
+    }
+    const float inv = SIGMOID ? 1.0f : __fdiv_rn(1.0f, fmaxf(total, FLT_MIN));
+    float top[SUB];                                 // the blocks' largest choices
+#pragma unroll
+    for (int j = 0; j < SUB; j++) {
+        const int s = l + LT * j;
+        top[j] = -INFINITY;
+        if (s < p.nsub) {
+            float f[8];
+            // A block whose logits, and whose choices with their bias, have a
+            // finite sum holds nothing that is off and no choice below -FLT_MAX:
+            // one test for eight.
+            bool plain = true;
+            if (SIGMOID) {
+                read8(row, s, f);
+                const float z = (f[0] + f[1]) + (f[2] + f[3]) + ((f[4] + f[5]) + (f[6] + f[7]));
+                plain = fabsf(z) < INFINITY;
+                float c[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) c[i] = quick_sigmoid(f[i]);
+                if (!plain) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (!(f[i] > -INFINITY)) c[i] = -FLT_MAX;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] = c[i];
+            } else {
+                get8(s, f);
+            }
+            if (p.bias) {
+                float c[8];
+                read8(p.bias, s, c);
+#pragma unroll
+                for (int i = 0; i < 8; i++) c[i] = fmaf(f[i], inv, c[i]);
+                const float z = (c[0] + c[1]) + (c[2] + c[3]) + ((c[4] + c[5]) + (c[6] + c[7]));
+                if (!plain || !(fabsf(z) < INFINITY) || !SIGMOID) {    // (softmax marks what is off by -FLT_MAX)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) c[i] = f[i] == -FLT_MAX ? f[i] : fmaxf(c[i], -FLT_MAX);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] = c[i];
+            }
+            if (!VEC) {
+                const int n = count(s);
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] = i < n ? f[i] : -INFINITY;
+            }
+            if (SIGMOID || p.bias || !VEC) put8(s, f);
+            top[j] = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+            if (groups) {                           // the best two, by pairs
+                float hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    hi[i] = fmaxf(f[2 * i], f[2 * i + 1]);
+                    lo[i] = fminf(f[2 * i], f[2 * i + 1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 3; i++) {       // 0+1, 2+3, then both
+                    const int x = i == 2 ? 0 : 2 * i, y = i == 2 ? 2 : 2 * i + 1;
+                    lo[x] = fmaxf(fmaxf(lo[x], lo[y]), fminf(hi[x], hi[y]));
+                    hi[x] = fmaxf(hi[x], hi[y]);
+                }
+                best_s[s] = make_float2(hi[0], lo[0]);
+            }
         }
     }
-    float w = 0.0f;
-    if (lane < p.K) {
-        const float z = logit<X>(row, chosen);
-        if (z > -INFINITY) w = SIGMOID ? sigmoid_f(z) : __fdiv_rn(soft_f(z, m), inv);
+    if (groups) {
+        // scores of groups l, l + LT, ...; then how many groups stand before each
+        __syncwarp();
+        constexpr int GL = 32 / LT;
+        float score[GL];
+        int before[GL];
+#pragma unroll
+        for (int i = 0; i < GL; i++) {
+            const int grp = l + LT * i;
+            float b1 = -INFINITY, b2 = -INFINITY;
+            if (grp < p.n_group)
+                for (int q = 0; q < p.spg.d; q++) {
+                    const float2 o = best_s[grp * p.spg.d + q];
+                    b2 = fmaxf(fmaxf(b2, o.y), fminf(b1, o.x));
+                    b1 = fmaxf(b1, o.x);
+                }
+            score[i] = p.best == 1 ? b1 : fmaxf(b1 + b2, -FLT_MAX);
+            before[i] = 0;
+        }
+        uint32_t kept = 0;
+#pragma unroll
+        for (int i = 0; i < GL; i++) {
+            if (LT * i >= p.n_group) break;
+#pragma unroll
+            for (int k = 0; k < LT; k++) {
+                const int other = k + LT * i;
+                const float o = __shfl_sync(0xffffffffu, score[i], (lane & ~(LT - 1)) + k);
+                if (other < p.n_group) {
+#pragma unroll
+                    for (int a = 0; a < GL; a++)
+                        before[a] += o > score[a] || (o == score[a] && other < l + LT * a);
+                }
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < GL; a++)
+            if (l + LT * a < p.n_group && before[a] < p.keep) kept |= 1u << (l + LT * a);
+#pragma unroll
+        for (int o = LT / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, o);
+#pragma unroll
+        for (int j = 0; j < SUB; j++) {
+            const int grp = p.spg.div(l + LT * j);
+            if (grp < p.n_group && !(kept >> grp & 1u)) top[j] = -INFINITY;
+        }
     }
-    if (p.renorm) {
-        const float sum = warp_sum(w, 32);
-        w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+
+    const uint32_t seg = LT == 32 ? 0xffffffffu : ((1u << (LT & 31)) - 1u) << (lane & ~(LT - 1));
+    for (int k = 0; k < p.K; k++) {
+        float v = top[0];                           // this lane's best block, the first of equals
+        int mine = 0;
+#pragma unroll
+        for (int j = 1; j < SUB; j++)
+            if (top[j] > v) {
+                v = top[j];
+                mine = j;
+            }
+        const int s = l + LT * mine;
+        const float best = lanes_max<LT>(v);
+        uint32_t who = __ballot_sync(0xffffffffu, v == best) & seg;
+        if (SUB > 1 && __any_sync(0xffffffffu, who & (who - 1))) {      // equal choices: the lowest block
+            int low = v == best ? s : INT32_MAX;
+#pragma unroll
+            for (int o = LT / 2; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+            who = __ballot_sync(0xffffffffu, v == best && s == low) & seg;
+        }
+        if (lane == __ffs(who) - 1) {
+            float f[8], n = 0.0f;
+            get8(s, f);
+            int at = 0;
+#pragma unroll
+            for (int i = 7; i >= 0; i--)
+                if (f[i] == best) {
+                    at = i;
+                    f[i] = -INFINITY;
+                    n += 1.0f;
+                }
+            float next = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+            if (n > 1.0f) next = best;              // its equals are left
+            c_s[(at >> 2) * NB * 4 + s * 4 + (at & 3)] = -INFINITY;
+            pick_s[k] = s * 8 + at;
+#pragma unroll
+            for (int j = 0; j < SUB; j++)
+                if (j == mine) top[j] = next;
+        }
     }
-    if (lane < p.K) {
-        p.idx[(size_t)t * p.K + lane] = chosen;
-        p.w[(size_t)t * p.K + lane] = w * p.factor;
+    __syncwarp();
+
+    constexpr int KL = (16 + LT - 1) / LT;
+    float w[KL], sum = 0.0f;
+    int e[KL];
+#pragma unroll
+    for (int i = 0; i < KL; i++) {
+        const int k = l + LT * i;
+        w[i] = 0.0f;
+        e[i] = 0;
+        if (k < p.K) {
+            e[i] = expert0(pick_s[k] >> 3) + (pick_s[k] & 7);
+            const float z = logit<X>(row, e[i]);
+            if (z > -INFINITY) w[i] = SIGMOID ? sigmoid_f(z) : __fdiv_rn(soft_f(z, m), total);
+        }
+        sum += w[i];
+    }
+    sum = lanes_sum<LT>(sum);
+#pragma unroll
+    for (int i = 0; i < KL; i++) {
+        const int k = l + LT * i;
+        if (!live || k >= p.K) continue;
+        const float v = p.renorm ? (sum > 0.0f ? __fdiv_rn(w[i], sum) : 0.0f) : w[i];
+        p.idx[(size_t)t * p.K + k] = e[i];
+        p.w[(size_t)t * p.K + k] = v * p.factor;
+    }
+}
+
+template <typename X, bool SIGMOID, int LT, int SUB>
+void launch_sub(const RouteParams &p, cudaStream_t st) {
+    constexpr int TOK = kRouteThreads / LT;
+    constexpr size_t smem = (size_t)TOK * route_token_floats(LT, SUB) * sizeof(float);
+    static_assert(smem <= 200 * 1024, "shared memory of a CTA");
+    auto kernel = p.vec ? scored_route_kernel<X, LT, SUB, SIGMOID, true> : scored_route_kernel<X, LT, SUB, SIGMOID, false>;
+    if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kernel<<<(unsigned)((p.T + TOK - 1) / TOK), kRouteThreads, smem, st>>>(p);
+}
+
+template <typename X, bool SIGMOID, int LT>
+void launch_lt(const RouteParams &p, cudaStream_t st) {
+    const int n = (p.nsub + LT - 1) / LT;             // blocks of a lane: 5 or 20 at most (E <= 1024, 32 groups)
+    if (n <= 1) return launch_sub<X, SIGMOID, LT, 1>(p, st);
+    if (n <= 2) return launch_sub<X, SIGMOID, LT, 2>(p, st);
+    if (n <= 4) return launch_sub<X, SIGMOID, LT, 4>(p, st);
+    if (LT == 32) return launch_sub<X, SIGMOID, LT, 5>(p, st);
+    if constexpr (LT == 8) {
+        if (n <= 8) return launch_sub<X, SIGMOID, LT, 8>(p, st);
+        if (n <= 16) return launch_sub<X, SIGMOID, LT, 16>(p, st);
+        return launch_sub<X, SIGMOID, LT, 20>(p, st);
     }
 }
 
 template <typename X, bool SIGMOID>
-void launch_nv(const RouteParams &p, int nv, cudaStream_t st) {
-    const int threads = 256;
-    const unsigned grid = (unsigned)((p.T + threads / 32 - 1) / (threads / 32));
-    if (nv <= 1) scored_route_kernel<X, 1, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else if (nv <= 2) scored_route_kernel<X, 2, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else if (nv <= 4) scored_route_kernel<X, 4, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else if (nv <= 8) scored_route_kernel<X, 8, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else if (nv <= 16) scored_route_kernel<X, 16, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else if (nv <= 32) scored_route_kernel<X, 32, SIGMOID><<<grid, threads, 0, st>>>(p);
-    else scored_route_kernel<X, 64, SIGMOID><<<grid, threads, 0, st>>>(p);
+void launch_route(const RouteParams &p, cudaStream_t st) {
+    // 32 lanes a token while that does not fill the SMs.  Measured, 32 against
+    // 8 lanes: 1 x 256 3.7 / 5.7 us, 2525 x 160 5.2 / 5.5, 4096 x 512 5.3 /
+    // 6.5, but 4433 x 60 5.4 / 3.2, 9028 x 64 9.1 / 3.8, 65521 x 256 80 / 35.
+    const int most = num_sms() * (p.nsub > 16 ? 32 : 8);
+    if (p.T <= most) launch_lt<X, SIGMOID, 32>(p, st);
+    else launch_lt<X, SIGMOID, 8>(p, st);
 }
 
 }  // namespace
@@ -211,26 +442,27 @@ extern "C" int moe_scored_route(const moe_route_desc *rd, const void *logits, in
     p.T = T;
     p.E = rd->E;
     p.K = rd->K;
-    p.n_group = rd->n_group;
-    p.gs = gs;
-    int np = 1;
-    while (np < rd->n_group) np *= 2;
-    p.lanes = 32 / np;
-    p.keep = rd->keep_group;
+    const bool groups = rd->keep_group < rd->n_group;     // all kept: as good as one group
+    p.n_group = groups ? rd->n_group : 1;
+    p.gs = groups ? gs : rd->E;
+    p.keep = groups ? rd->keep_group : 1;
+    p.spg = FastDiv((p.gs + 7) / 8);
+    p.nsub = p.n_group * p.spg.d;
     p.best = rd->group_best;
     p.renorm = rd->renorm != 0;
+    p.vec = p.gs % 8 == 0 && stride * elt % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+            reinterpret_cast<uintptr_t>(rd->bias) % 16 == 0;
     p.factor = rd->factor;
     p.bias = rd->bias;
     p.idx = idx;
     p.w = w;
-    const int nv = (gs + p.lanes - 1) / p.lanes;      // at most 61: E <= 1024
     const bool sig = rd->score == MOE_SCORE_SIGMOID;
     if (logits_dtype == MOE_DTYPE_F32) {
-        if (sig) launch_nv<float, true>(p, nv, stream);
-        else launch_nv<float, false>(p, nv, stream);
+        if (sig) launch_route<float, true>(p, stream);
+        else launch_route<float, false>(p, stream);
     } else {
-        if (sig) launch_nv<__nv_bfloat16, true>(p, nv, stream);
-        else launch_nv<__nv_bfloat16, false>(p, nv, stream);
+        if (sig) launch_route<__nv_bfloat16, true>(p, stream);
+        else launch_route<__nv_bfloat16, false>(p, stream);
     }
     return check_launch("scored_route_kernel");
 }
