@@ -27,10 +27,14 @@ int check_launch(const char *what) {
 }
 
 int num_sms() {
+    static std::atomic<int> known[64];            // 0: not asked yet
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 1;
+    if (n <= 0) return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 static bool aligned(const void *p, size_t a) {

@@ -47,6 +47,8 @@ extern "C" int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_d
                     window);
     if (q_dtype != MOE_DTYPE_F32 && q_dtype != MOE_DTYPE_BF16)
         return fail(MOE_EINVAL, "paged_attention: q_dtype=%d", q_dtype);
+    if ((int64_t)B * Hq > INT32_MAX)
+        return fail(MOE_EUNSUPPORTED, "paged_attention: B=%d Hq=%d (need fewer than 2^31 rows)", B, Hq);
     if (!(scale > 0.0f) || !(scale < INFINITY))
         return fail(MOE_EINVAL, "paged_attention: scale=%g (need a positive number)", (double)scale);
     if (B == 0) return MOE_OK;
@@ -86,7 +88,6 @@ extern "C" int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_d
     p.table = block_table;
     p.max_blocks = max_blocks;
     p.window = window;
-    p.ctas = wl.ctas;
     p.scale = scale;
     p.out = out;
     p.lse = lse;

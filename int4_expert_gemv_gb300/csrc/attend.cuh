@@ -56,9 +56,7 @@
 namespace moe {
 
 constexpr int kAttWarps = 4;
-constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kAttTile = 16;                          // tokens of a warp's tile
-constexpr int kAttUnit = kAttTile * kAttWarps;        // tokens of a unit of work
 
 constexpr int kMaxLength = INT32_MAX - 65535;         // places past the last tile stay in 32 bits
 
@@ -73,11 +71,11 @@ struct AttendParams {
     size_t q_stride, out_stride;
     int Hq;
     const int32_t *seq, *table;
-    int max_blocks, window, ctas;
+    int max_blocks, window, ctas, by_row, whole;
     float scale;
     void *out;
     float *lse;
-    int4 *meta;                      // [ctas]: a row that starts in the CTA and goes on (pieces, request, head tile, first slot)
+    int4 *meta;                      // rows in several parts: {parts, row, first CTA, its slot}, by row or by first CTA
     float2 *part_ml;                 // [2 ctas][rows]
     float *part_o;                   // [2 ctas][rows][DP]
 };
@@ -91,6 +89,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
                  : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -158,6 +159,7 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
 
 template <int DP, bool F8, bool QF32, bool FULL>
 struct AttendShape {
+    static constexpr int NW = kAttWarps;
     static constexpr int ELT = F8 ? 1 : 2;
     static constexpr int CH = DP * ELT / 16;                  // 16-byte chunks of a row
     static constexpr int NQ = QF32 ? (F8 ? 2 : 3) : 1;        // parts of q
@@ -168,14 +170,20 @@ struct AttendShape {
     static constexpr int STEPS = DP / 16;
     static constexpr int TILE_B = kAttTile * DP * ELT;        // bytes of a tile's keys (or values)
     static constexpr int STAGE = 2 * TILE_B;
-    // Stages and CTAs per SM: 96 to 192 KB of stages per SM, two of three or
-    // more in flight.
-    static constexpr int NS = F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3) : (DP == 64 ? 6 : DP == 192 ? 4 : 3);
-    static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP <= 128 ? 2 : 1);
+    // Stages and CTAs per SM, of the shared memory (192 KB of stages) and the
+    // registers.  More CTAs hide a tile's own latencies better, more stages
+    // the memory's: with an fp32 q in up to 8 rows (more products a tile)
+    // three CTAs of two stages beat two of three (29 windows of 1000: 39
+    // against 44 us; 64 ragged bf16 requests: 153 against 152).
+    static constexpr bool BUSY = QF32 && !FULL;
+    static constexpr int NS = F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3) : (DP == 128 ? (BUSY ? 2 : 3) : DP == 256 ? 3 : 4);
+    static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP == 64 ? 3 : DP == 128 ? (BUSY ? 3 : 2) : 1);
+    static constexpr int THREADS = 32 * NW, UNIT = kAttTile * NW;
     static constexpr int RING = NS * STAGE;                   // of one warp
-    static constexpr int Q_B = NA * STEPS * 512;
+    static constexpr bool HALF = !FULL && NQ == 1;            // operand rows 8-15 of q are zero and not stored
+    static constexpr int Q_B = NA * STEPS * (HALF ? 256 : 512);
     static constexpr int LDO = DP + 4;                        // floats of a row of O in the join of the warps
-    static constexpr int SMEM = kAttWarps * RING + Q_B;
+    static constexpr int SMEM = NW * RING + Q_B;
     static_assert(ROWS * LDO * 4 <= RING, "a warp's O fits its ring");
 };
 
@@ -192,11 +200,17 @@ __device__ __forceinline__ uint32_t value_at(int r, int c) {
     return (uint32_t)(pos * CH + (c ^ (pos & 2))) * 16;
 }
 
+template <int UNIT>
 __device__ __forceinline__ int units_of(int len, int window, int room) {
     len = min(len, room);
     if (len <= 0) return 0;
     const int lo = window > 0 && len > window ? (len - window) & ~(kAttTile - 1) : 0;
-    return (len - lo + kAttUnit - 1) / kAttUnit;
+    return (len - lo + UNIT - 1) / UNIT;
+}
+
+// Quotient of a 64-bit number that nearly always fits 32 bits.
+__device__ __forceinline__ int quotient(int64_t a, int b) {
+    return a >> 31 ? (int)(a / b) : (int)a / b;
 }
 
 template <bool QF32>
@@ -212,29 +226,29 @@ __device__ __forceinline__ void store4(void *out, size_t i, float4 f) {
 
 // ---------------------------------------------------------------- kernel
 template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
-__global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>::CTAS))
+__global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FULL>::CTAS))
     attend_kernel(const AttendParams p) {
     using S = AttendShape<DP, F8, QF32, FULL>;
-    constexpr int CH = S::CH, NS = S::NS, ROWS = S::ROWS, R = FULL ? 2 : 1;
+    constexpr int NW = S::NW, CH = S::CH, NS = S::NS, ROWS = S::ROWS, R = FULL ? 2 : 1, THREADS = S::THREADS, UNIT = S::UNIT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sm_sum[kAttWarps];
+    __shared__ int64_t sm_sum[NW];
     __shared__ int64_t sm_off;
     __shared__ int sm_b, sm_bad;
     __shared__ float sm_c[16];
-    __shared__ float2 sm_ml[kAttWarps][16];
+    __shared__ float2 sm_ml[NW][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int cta = blockIdx.x, HT = p.Hkv * p.tiles;
     const int room = (int)min((int64_t)p.max_blocks * p.page.d, (int64_t)kMaxLength);
     asm volatile("griddepcontrol.launch_dependents;");   // the join may take the SMs as they empty
     uint8_t *ring = smem + warp * S::RING;
     const uint32_t ring_a = smem_addr(ring);
-    uint4 *q_s = reinterpret_cast<uint4 *>(smem + kAttWarps * S::RING);
+    uint8_t *q_s = smem + NW * S::RING;
 
     // where this CTA's run begins
-    const int run = (p.B + kAttThreads - 1) / kAttThreads;
+    const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     int64_t sum = 0;
-    for (int b = b0; b < b1; b++) sum += units_of(p.seq[b], p.window, room);
+    for (int b = b0; b < b1; b++) sum += units_of<UNIT>(p.seq[b], p.window, room);
     int64_t before = sum;
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, before, o);
@@ -242,17 +256,18 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
     }
     if (lane == 31) sm_sum[warp] = before;
     before -= sum;
-    for (int i = tid; i < S::Q_B / 16; i += kAttThreads) q_s[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < S::Q_B / 16; i += THREADS) reinterpret_cast<uint4 *>(q_s)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     int64_t W = 0;
 #pragma unroll
-    for (int w = 0; w < kAttWarps; w++) {
+    for (int w = 0; w < NW; w++) {
         if (w == warp) before += W;
         W += sm_sum[w];
     }
     W *= HT;
-    const int n_cta = (int)min((int64_t)p.ctas, W);
-    if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
+    // a unit for each CTA while that makes at most 64 parts of a row, then four
+    const int n_cta = (int)min((int64_t)p.ctas, max(W / 4, min(W, (int64_t)p.B * HT * 64)));
+    if (tid == 0 && !p.by_row && !p.whole) p.meta[cta] = make_int4(0, 0, 0, 0);
     int64_t u0 = 0, u1 = 0;
     if (cta < n_cta) {
         u0 = cta * W / n_cta;
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
             int64_t at = before;
             int b = b0;
             for (;; b++) {
-                const int n = units_of(p.seq[b], p.window, room);
+                const int n = units_of<UNIT>(p.seq[b], p.window, room);
                 if (u0 < (at + n) * HT) break;
                 at += n;
             }
@@ -276,47 +291,131 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
     bool first_seg = true;
     for (int64_t u = u0; u < u1;) {
         const int full_len = p.seq[b];
-        const int nb = units_of(full_len, p.window, room);
+        const int nb = units_of<UNIT>(full_len, p.window, room);
         if (off >= (int64_t)nb * HT) {
             off = 0;
             b++;
             continue;
         }
-        const int ht = (int)(off / nb), blk = (int)(off - (int64_t)ht * nb);
-        const int n_unit = (int)min((int64_t)(nb - blk), u1 - u);
+        const int ht = quotient(off, nb), blk = (int)(off - (int64_t)ht * nb);
+        if (p.whole && blk > 0) {              // the row belongs to the CTA that its first unit fell to
+            off += nb - blk;
+            u += nb - blk;
+            continue;
+        }
+        const int n_unit = p.whole ? nb : (int)min((int64_t)(nb - blk), u1 - u);
         const int h = ht / p.tiles, head0 = h * p.G + (ht - h * p.tiles) * ROWS;
         const int n_rows = min(ROWS, (h + 1) * p.G - head0);
         const int len = min(full_len, room);
         const int lo = p.window > 0 ? max(0, len - p.window) : 0;
-        const int tile0 = (lo & ~(kAttTile - 1)) + blk * kAttUnit;      // this segment's first token
-        const int stop = min(len, tile0 + n_unit * kAttUnit);
+        const int tile0 = (lo & ~(kAttTile - 1)) + blk * UNIT;      // this segment's first token
+        const int stop = min(len, tile0 + n_unit * UNIT);
         const int n_tile = (stop - tile0 + kAttTile - 1) / kAttTile;
-        const int mine = n_tile > warp ? (n_tile - warp + kAttWarps - 1) / kAttWarps : 0;
+        const int mine = n_tile > warp ? (n_tile - warp + NW - 1) / NW : 0;
         if (tid == 0) sm_bad = full_len > room;
 
-        // ---- q: split into parts, in the order of the operand's registers
-        const float c0 = p.scale * 1.44269504088896341f * (F8 && p.k_scale ? p.k_scale[h] : 1.0f);
-        for (int r = warp; r < ROWS; r += kAttWarps) {
-            constexpr int IT = (DP / 4 + 31) / 32;
-            float x[IT][4];
-            float top = 0.0f;
+        // ---- q: the numbers are loaded before the first tiles are asked for, and split after
+        constexpr int QR = ROWS / NW, IT = (DP / 4 + 31) / 32;
+        uint4 qx[QR][IT];
+#pragma unroll
+        for (int k = 0; k < QR; k++)
 #pragma unroll
             for (int i = 0; i < IT; i++) {
-                const int d = 4 * (lane + 32 * i);
-                x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
+                const int r = warp + NW * k, d = 4 * (lane + 32 * i);
+                qx[k][i] = make_uint4(0, 0, 0, 0);
                 if (d < p.D && r < n_rows) {
                     const size_t at = (size_t)b * p.q_stride + (size_t)(head0 + r) * p.D + d;
                     if (QF32) {
-                        const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
-                        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+                        qx[k][i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + at));
                     } else {
-                        const uint2 f = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + at);
-                        x[i][0] = __uint_as_float(f.x << 16), x[i][1] = __uint_as_float(f.x & 0xffff0000u);
-                        x[i][2] = __uint_as_float(f.y << 16), x[i][3] = __uint_as_float(f.y & 0xffff0000u);
+                        const uint2 f = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + at));
+                        qx[k][i] = make_uint4(f.x << 16, f.x & 0xffff0000u, f.y << 16, f.y & 0xffff0000u);
                     }
                 }
+            }
+        const float c0 = p.scale * 1.44269504088896341f * (F8 && p.k_scale ? __ldg(p.k_scale + h) : 1.0f);
+
+        // ---- the warp's tiles
+        const int row_b = p.D * S::ELT;                            // bytes of a stored row
+        const size_t head_b = (size_t)h * p.page.d * row_b;
+        const int32_t *tab = p.table + (size_t)b * p.max_blocks;
+        int ids = 0, ids8 = 0;          // ALIGNED: the pages of 32 tiles; else of rows lane / 4 and 8 more of the next tile
+        bool bad = false;
+        auto page_of = [&](int tok) { return tok < stop ? __ldg(tab + p.page.div(tok)) : -1; };
+        auto fetch_ids = [&](int i) {   // before tile i is issued
+            if (ALIGNED) {
+                if ((i & 31) == 0) ids = page_of(tile0 + (warp + NW * (i + lane)) * kAttTile);
+            } else {
+                const int tok = tile0 + (warp + NW * i) * kAttTile + g;
+                ids = page_of(tok);
+                ids8 = page_of(tok + 8);
+            }
+        };
+        auto issue = [&](int i) {
+            if (i < mine) {
+                const int tok0 = tile0 + (warp + NW * i) * kAttTile;
+                const uint32_t dst = ring_a + (i % NS) * S::STAGE;
+                if (ALIGNED) {          // one page: whole rows, row after row
+                    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+                    const bool ok0 = (unsigned)id < (unsigned)p.n_pages;
+                    const int in = tok0 - p.page.div(tok0) * p.page.d;
+                    bad |= !ok0;
+                    fetch_ids(i + 1);
+                    const size_t at0 = (ok0 ? (size_t)id : 0) * p.page_stride + head_b + (size_t)in * row_b;
+                    const uint8_t *k0 = p.k + at0, *v0 = p.v + at0;
+                    if (ok0 && tok0 >= lo && tok0 + kAttTile <= stop && row_b == CH * 16) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) top = fmaxf(top, fabsf(x[i][j]));
+                        for (int n = 0; n < CH * kAttTile / 32; n++) {
+                            const int e = n * 32 + lane, r = e / CH, ch = e - r * CH;
+                            copy16(dst + key_at<CH>(r, ch), k0 + e * 16);
+                            copy16(dst + S::TILE_B + value_at<CH>(r, ch), v0 + e * 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < CH * kAttTile / 32; n++) {
+                            const int e = n * 32 + lane, r = e / CH, ch = e - r * CH, tok = tok0 + r;
+                            const bool ok = ok0 && tok >= lo && tok < stop && ch * 16 < row_b;
+                            const int at = ok ? r * row_b + ch * 16 : 0;
+                            copy16(dst + key_at<CH>(r, ch), ok ? k0 + at : p.k, ok);
+                            copy16(dst + S::TILE_B + value_at<CH>(r, ch), ok ? v0 + at : p.v, ok);
+                        }
+                    }
+                } else {                // a page per row: four lanes a row, two rows a lane
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        const int r = g + 8 * hf, tok = tok0 + r, id = hf ? ids8 : ids;
+                        const bool in_page = (unsigned)id < (unsigned)p.n_pages, seen = tok >= lo && tok < stop;
+                        const bool ok0 = in_page && seen;
+                        bad |= seen && !in_page;
+                        const int in = tok - p.page.div(tok) * p.page.d;
+                        const size_t at0 = ok0 ? (size_t)id * p.page_stride + head_b + (size_t)in * row_b : 0;
+#pragma unroll
+                        for (int n = 0; n < CH / 4; n++) {
+                            const int ch = 4 * n + t;
+                            const bool ok = ok0 && ch * 16 < row_b;
+                            const size_t at = ok ? at0 + ch * 16 : 0;
+                            copy16(dst + key_at<CH>(r, ch), p.k + at, ok);
+                            copy16(dst + S::TILE_B + value_at<CH>(r, ch), p.v + at, ok);
+                        }
+                    }
+                    fetch_ids(i + 1);
+                }
+            }
+            copy_commit();
+        };
+        fetch_ids(0);
+#pragma unroll
+        for (int i = 0; i < NS - 1; i++) issue(i);
+        // ---- q, split into parts in the order of the operand's registers
+#pragma unroll
+        for (int k = 0; k < QR; k++) {
+            const int r = warp + NW * k;
+            float top = 0.0f;
+            if (F8) {
+#pragma unroll
+                for (int i = 0; i < IT; i++)
+                    top = fmaxf(fmaxf(fmaxf(top, fabsf(__uint_as_float(qx[k][i].x))), fabsf(__uint_as_float(qx[k][i].y))),
+                                fmaxf(fabsf(__uint_as_float(qx[k][i].z)), fabsf(__uint_as_float(qx[k][i].w))));
             }
             float f = c0 < 0.0f ? -1.0f : 1.0f, c = fabsf(c0);
             if (F8) {                     // fp16 parts: the row's largest number to 2^13 .. 2^14
@@ -334,14 +433,15 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
                 if (d >= DP) break;
                 const int per = F8 ? 16 : 8;                       // numbers of a lane in a unit of the row
                 const int step = d / (4 * per) * (per / 4) + d % per / 4, tt = d / per % 4;
-#pragma unroll
-                for (int j = 0; j < 4; j++) x[i][j] *= f;
+                float x[4] = {__uint_as_float(qx[k][i].x) * f, __uint_as_float(qx[k][i].y) * f,
+                              __uint_as_float(qx[k][i].z) * f, __uint_as_float(qx[k][i].w) * f};
 #pragma unroll
                 for (int part = 0; part < S::NQ; part++) {
                     const int na = FULL ? part : part / 2, up = FULL ? r >> 3 : part & 1;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(q_s + (na * S::STEPS + step) * 32 + (r & 7) * 4 + tt);
-                    w[up] = pair_of<F8>(x[i][0], x[i][1]);
-                    w[2 + up] = pair_of<F8>(x[i][2], x[i][3]);
+                    constexpr int W = S::HALF ? 2 : 4;            // words of a lane
+                    uint32_t *w = reinterpret_cast<uint32_t *>(q_s) + ((na * S::STEPS + step) * 32 + (r & 7) * 4 + tt) * W;
+                    w[up] = pair_of<F8>(x[0], x[1]);
+                    w[W / 2 + up] = pair_of<F8>(x[2], x[3]);
                 }
             }
         }
@@ -357,72 +457,15 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
 #pragma unroll
         for (int i = 0; i < DP / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-        // ---- the warp's tiles
-        const int row_b = p.D * S::ELT;                            // bytes of a stored row
-        const size_t head_b = (size_t)h * p.page.d * row_b;
-        const int32_t *tab = p.table + (size_t)b * p.max_blocks;
-        int ids = 0;                    // ALIGNED: the pages of 32 tiles; else of the next tile's rows
-        bool bad = false;
-        auto page_of = [&](int tok) { return tok < stop ? tab[p.page.div(tok)] : -1; };
-        auto fetch_ids = [&](int i) {   // before tile i is issued
-            if (ALIGNED) {
-                if ((i & 31) == 0) ids = page_of(tile0 + (warp + kAttWarps * (i + lane)) * kAttTile);
-            } else {
-                ids = page_of(tile0 + (warp + kAttWarps * i) * kAttTile + (lane & 15));
-            }
-        };
-        auto issue = [&](int i) {
-            if (i < mine) {
-                const int tok0 = tile0 + (warp + kAttWarps * i) * kAttTile;
-                const uint32_t dst = ring_a + (i % NS) * S::STAGE;
-                size_t base = 0;
-                bool ok0 = false;
-                if (ALIGNED) {
-                    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-                    ok0 = (unsigned)id < (unsigned)p.n_pages;
-                    const int in = tok0 - p.page.div(tok0) * p.page.d;
-                    base = (ok0 ? (size_t)id : 0) * p.page_stride + head_b + (size_t)in * row_b;
-                    bad |= !ok0;
-                    fetch_ids(i + 1);
-                } else {
-                    const int tok = tok0 + (lane & 15);
-                    ok0 = (unsigned)ids < (unsigned)p.n_pages;
-                    bad |= !ok0 && tok >= lo && tok < stop;
-                    const int in = tok - p.page.div(tok) * p.page.d;
-                    base = (ok0 ? (size_t)ids : 0) * p.page_stride + head_b + (size_t)in * row_b;
-                    fetch_ids(i + 1);
-                }
-#pragma unroll
-                for (int n = 0; n < CH * kAttTile / 32; n++) {
-                    const int e = n * 32 + lane, r = e / CH, ch = e - r * CH;
-                    size_t at = base + (size_t)(r * row_b);
-                    bool ok = ok0;
-                    if (!ALIGNED) {
-                        at = __shfl_sync(0xffffffffu, (unsigned long long)base, r);
-                        ok = __shfl_sync(0xffffffffu, (int)ok0, r);
-                    }
-                    at += ch * 16;
-                    const int tok = tok0 + r;
-                    ok = ok && tok >= lo && tok < stop && ch * 16 < row_b;
-                    at = ok ? at : 0;
-                    copy16(dst + key_at<CH>(r, ch), p.k + at, ok);
-                    copy16(dst + S::TILE_B + value_at<CH>(r, ch), p.v + at, ok);
-                }
-            }
-            copy_commit();
-        };
-        fetch_ids(0);
-#pragma unroll
-        for (int i = 0; i < NS - 1; i++) issue(i);
         for (int i = 0; i < mine; i++) {
             __syncwarp();
             issue(i + NS - 1);
             copy_wait<NS - 1>();
             __syncwarp();
             const uint32_t ks = ring_a + (i % NS) * S::STAGE, vs = ks + S::TILE_B;
-            const int tok0 = tile0 + (warp + kAttWarps * i) * kAttTile;
+            const int tok0 = tile0 + (warp + NW * i) * kAttTile;
 
-            float s[2][4] = {};
+            float sp[2][2][4] = {};                 // two chains of products for each 8 tokens
 #pragma unroll
             for (int un = 0; un < CH / 4; un++) {
                 const uint4 k0 = lds16(ks + key_at<CH>(g, 4 * un + t));
@@ -441,12 +484,24 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
                     }
 #pragma unroll
                     for (int na = 0; na < S::NA; na++) {
-                        const uint4 a = q_s[(na * S::STEPS + step) * 32 + lane];
-                        mma<F8>(s[0], a.x, a.y, a.z, a.w, x0, x1);
-                        mma<F8>(s[1], a.x, a.y, a.z, a.w, y0, y1);
+                        float(*s)[4] = sp[(step + na) & 1];
+                        if (S::HALF) {
+                            const uint2 a = reinterpret_cast<const uint2 *>(q_s)[(na * S::STEPS + step) * 32 + lane];
+                            mma<F8>(s[0], a.x, 0u, a.y, 0u, x0, x1);
+                            mma<F8>(s[1], a.x, 0u, a.y, 0u, y0, y1);
+                        } else {
+                            const uint4 a = reinterpret_cast<const uint4 *>(q_s)[(na * S::STEPS + step) * 32 + lane];
+                            mma<F8>(s[0], a.x, a.y, a.z, a.w, x0, x1);
+                            mma<F8>(s[1], a.x, a.y, a.z, a.w, y0, y1);
+                        }
                     }
                 }
             }
+            float s[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) s[n][j] = sp[0][n][j] + sp[1][n][j];
             // x[r][4]: tokens 2t, 2t+1, 2t+8, 2t+9 of head g (and g + 8)
             float x[R][4];
 #pragma unroll
@@ -586,15 +641,15 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
         const bool whole = n_unit == nb;
         const float v_scale = F8 && p.v_scale ? p.v_scale[h] : 1.0f;
         const int slot = 2 * cta + (first_seg ? 0 : 1);
-        for (int i = tid; i < n_rows * (DP / 4); i += kAttThreads) {
+        for (int i = tid; i < n_rows * (DP / 4); i += THREADS) {
             const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
             float M = -INFINITY, L = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kAttWarps; w++) M = fmaxf(M, sm_ml[w][r].x);
+            for (int w = 0; w < NW; w++) M = fmaxf(M, sm_ml[w][r].x);
             const float ref = M == -INFINITY ? 0.0f : M;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kAttWarps; w++) {
+            for (int w = 0; w < NW; w++) {
                 const float2 ml = sm_ml[w][r];
                 const float fw = exp2_f(ml.x - ref);
                 const float4 e = *reinterpret_cast<const float4 *>(
@@ -620,7 +675,9 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
         if (tid == 0 && blk == 0 && n_unit < nb) {
             const int64_t last = u + nb - 1;                       // the row's last unit, and its CTA
             const int c1 = (int)(((last + 1) * n_cta - 1) / W);
-            p.meta[cta] = make_int4(c1 - cta + 1, b, ht, slot);
+            p.meta[p.by_row ? b * HT + ht : cta] = make_int4(c1 - cta + 1, b * HT + ht, cta, slot);
+        } else if (tid == 0 && blk == 0 && p.by_row && !p.whole) {
+            p.meta[b * HT + ht] = make_int4(0, 0, 0, 0);
         }
         __syncthreads();
         first_seg = false;
@@ -630,67 +687,75 @@ __global__ void __launch_bounds__(kAttThreads, (AttendShape<DP, F8, QF32, FULL>:
 
     // rows with nothing to see
     for (int e = cta; e < p.B; e += gridDim.x) {
-        if (units_of(p.seq[e], p.window, room) > 0) continue;
-        for (int i = tid; i < p.Hq * p.D / 4; i += kAttThreads)
+        if (units_of<UNIT>(p.seq[e], p.window, room) > 0) continue;
+        for (int i = tid; i < p.Hq * p.D / 4; i += THREADS)
             store4<QF32>(p.out, (size_t)e * p.out_stride + 4 * (size_t)i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         if (p.lse)
-            for (int i = tid; i < p.Hq; i += kAttThreads) p.lse[(size_t)e * p.Hq + i] = -INFINITY;
+            for (int i = tid; i < p.Hq; i += THREADS) p.lse[(size_t)e * p.Hq + i] = -INFINITY;
+        if (p.by_row && !p.whole)
+            for (int i = tid; i < HT; i += THREADS) p.meta[e * HT + i] = make_int4(0, 0, 0, 0);
     }
 }
 
-// Joins a row's parts, one CTA per (CTA of the row's first part, head): the
-// warps take every eighth part, their lanes four dimensions each.
-template <bool QF32>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int dp, int rows) {
-    __shared__ float4 acc_s[8][64];
-    __shared__ float red[8];
+// Joins a row's parts, one CTA per (row in several parts, head): warp w takes
+// every JW-th part, its lanes four dimensions each.
+template <bool QF32, int JW>
+__global__ void __launch_bounds__(32 * JW) attend_join_kernel(const AttendParams p, int dp, int rows) {
+    __shared__ float4 acc_s[JW][64];
+    __shared__ float2 ml_s[JW];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 meta = p.meta[blockIdx.x];
-    const int n = meta.x, b = meta.y, r = blockIdx.y;
+    const int n = meta.x, HT = p.Hkv * p.tiles, r = blockIdx.y;
     if (n == 0) return;
-    const int h = meta.z / p.tiles, head0 = h * p.G + (meta.z - h * p.tiles) * rows;
+    const int b = meta.y / HT, ht = meta.y - b * HT, h = ht / p.tiles, head0 = h * p.G + (ht - h * p.tiles) * rows;
     if (head0 + r >= (h + 1) * p.G) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto slot = [&](int j) { return j == 0 ? (size_t)meta.w : 2 * ((size_t)blockIdx.x + j); };
-    float M = -INFINITY;
-    for (int j = tid; j < n; j += 256) M = fmaxf(M, p.part_ml[slot(j) * rows + r].x);
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
-    for (int w = 0; w < 8; w++) M = fmaxf(M, red[w]);
-    __syncthreads();
-    const float ref = M == -INFINITY ? 0.0f : M;
-    const int q = dp / 4;                            // float4s of a row: 16 .. 64
-    float L = 0.0f;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = dp / 4;      // float4s of a row: 16 .. 64
+    auto slot = [&](int j) { return (j == 0 ? (size_t)meta.w : 2 * ((size_t)meta.z + j)) * rows + r; };
+    float M = -INFINITY, L = 0.0f;
     float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-#pragma unroll 4
-    for (int j = warp; j < n; j += 8) {
-        const size_t s = slot(j) * rows + r;
-        const float2 ml = p.part_ml[s];
-        const float f = exp2_f(ml.x - ref);
-        L = fmaf(f, ml.y, L);
+    for (int j0 = warp; j0 < n; j0 += 32 * JW) {      // 32 parts of this warp: their (m, l), one a lane
+        const int jl = j0 + JW * lane;
+        const float2 ml = jl < n ? p.part_ml[slot(jl)] : make_float2(-INFINITY, 0.0f);
+        float top = ml.x;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.0f : Mn;
+        const float old = exp2_f(M - ref), f = exp2_f(ml.x - ref);
+        M = Mn;
+        L = fmaf(L, old, warp_sum(f * ml.y, 32));
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            if (lane + 32 * i < q) {
-                const float4 e = *reinterpret_cast<const float4 *>(p.part_o + s * dp + 4 * (lane + 32 * i));
-                acc[i].x = fmaf(f, e.x, acc[i].x);
-                acc[i].y = fmaf(f, e.y, acc[i].y);
-                acc[i].z = fmaf(f, e.z, acc[i].z);
-                acc[i].w = fmaf(f, e.w, acc[i].w);
+        for (int i = 0; i < 2; i++) acc[i].x *= old, acc[i].y *= old, acc[i].z *= old, acc[i].w *= old;
+        const int m = min(32, (n - j0 + JW - 1) / JW);
+#pragma unroll 8
+        for (int i = 0; i < m; i++) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            const float *o = p.part_o + slot(j0 + JW * i) * dp;
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                if (lane + 32 * c < q) {
+                    const float4 e = __ldcg(reinterpret_cast<const float4 *>(o) + lane + 32 * c);
+                    acc[c].x = fmaf(fi, e.x, acc[c].x);
+                    acc[c].y = fmaf(fi, e.y, acc[c].y);
+                    acc[c].z = fmaf(fi, e.z, acc[c].z);
+                    acc[c].w = fmaf(fi, e.w, acc[c].w);
+                }
             }
         }
     }
     acc_s[warp][lane] = acc[0];
     acc_s[warp][lane + 32] = acc[1];
-    if (lane == 0) red[warp] = L;
+    if (lane == 0) ml_s[warp] = make_float2(M, L);
     __syncthreads();
     if (tid < q && 4 * tid < p.D) {
+        M = -INFINITY;
+        for (int w = 0; w < JW; w++) M = fmaxf(M, ml_s[w].x);
+        const float ref = M == -INFINITY ? 0.0f : M;
         float4 a = make_float4(0, 0, 0, 0);
         L = 0.0f;
-        for (int w = 0; w < 8; w++) {
+        for (int w = 0; w < JW; w++) {
+            const float f = exp2_f(ml_s[w].x - ref);
             const float4 e = acc_s[w][tid];
-            a.x += e.x, a.y += e.y, a.z += e.z, a.w += e.w;
-            L += red[w];
+            a.x = fmaf(f, e.x, a.x), a.y = fmaf(f, e.y, a.y), a.z = fmaf(f, e.z, a.z), a.w = fmaf(f, e.w, a.w);
+            L = fmaf(f, ml_s[w].y, L);
         }
         const float inv = (p.v_scale ? p.v_scale[h] : 1.0f) / L;
         store4<QF32>(p.out, (size_t)b * p.out_stride + (size_t)(head0 + r) * p.D + 4 * tid,
@@ -701,30 +766,46 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
 
 // ---------------------------------------------------------------- launch
 template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
-int launch_attend_kernel(const AttendParams &p, cudaStream_t st) {
+int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     using S = AttendShape<DP, F8, QF32, FULL>;
     auto kernel = attend_kernel<DP, F8, QF32, FULL, ALIGNED>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    p.ctas = num_sms() * S::CTAS;
+    const int64_t rows = (int64_t)p.B * p.Hkv * p.tiles;
+    p.by_row = rows <= p.ctas;
+    // Rows of at most four units (by the table's width and the window) are
+    // not cut: a CTA takes those that begin in its run, which costs less than
+    // the join and its launch.
+    const int64_t room = (int64_t)p.max_blocks * p.page.d;
+    const int64_t longest = p.window > 0 && p.window + kAttTile < room ? p.window + kAttTile : room;
+    p.whole = longest <= 4 * S::UNIT;
+    static OnDevices ready;
+    cudaError_t e = ready.once([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    });
     if (e == cudaSuccess) {
-        kernel<<<p.ctas, kAttThreads, S::SMEM, st>>>(p);
+        kernel<<<p.ctas, S::THREADS, S::SMEM, st>>>(p);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_kernel: %s", cudaGetErrorString(e));
+    if (p.whole) return MOE_OK;
+    // few rows: many parts each, so many warps; else a small CTA that mostly finds nothing to do
+    const bool few = rows * 8 <= p.ctas;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)min(S::ROWS, p.G));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(p.by_row ? rows : p.ctas), (unsigned)min(S::ROWS, p.G));
+    cfg.blockDim = dim3(few ? 512 : 256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32>, p, DP, (int)S::ROWS);
+    e = few ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 16>, p, DP, (int)S::ROWS)
+            : cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 8>, p, DP, (int)S::ROWS);
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_join_kernel: %s", cudaGetErrorString(e));
     return MOE_OK;
 }
 
-// CTAs per SM, padded head size and tile rows of a shape; the workspace goes by them.
+// Padded head size, tile rows and most CTAs per SM of a shape; the workspace goes by them.
 struct AttendPlan {
     int dp, rows, ctas_per_sm;
 };
@@ -732,7 +813,7 @@ inline AttendPlan attend_plan(int D, bool f8, int G) {
     AttendPlan a;
     a.dp = D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 && !f8 ? 192 : 256;
     a.rows = G > 8 ? 16 : 8;
-    a.ctas_per_sm = f8 ? (a.dp == 256 ? 2 : 3) : (a.dp <= 128 ? 2 : 1);
+    a.ctas_per_sm = f8 ? (a.dp == 256 ? 2 : 3) : (a.dp <= 128 ? 3 : 1);
     return a;
 }
 

@@ -3,6 +3,7 @@
 // enqueues work; it returns a moe_status.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -86,7 +87,27 @@ int launch_debug_dequant(const uint8_t *sec, size_t rec, size_t first_record,
                          size_t record_step, int rows, int cols, int bits, float *out,
                          cudaStream_t st);
 
-int num_sms();
+int num_sms();                       // of the current device
+
+// Something to be done once on each device (a kernel's attributes): runs f on
+// the current device unless it has succeeded there before.  Devices past the
+// 64th run it every time.
+class OnDevices {
+  public:
+    template <typename F>
+    cudaError_t once(F f) {
+        int dev = 0;
+        if (cudaError_t e = cudaGetDevice(&dev)) return e;
+        const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        const cudaError_t e = f();
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+
+  private:
+    std::atomic<uint64_t> done_{0};
+};
 
 // Validation of a decode-stack descriptor shared by the decode-step paths.
 int check_decode_stack(const moe_stack_desc *sd);

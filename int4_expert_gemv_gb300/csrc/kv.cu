@@ -342,8 +342,11 @@ extern "C" int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R
                        pool, seq_out, first, slots, places, cap, pool_out, status};
     const size_t smem = 3 * (size_t)(R + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static OnDevices ready;
+        const cudaError_t e = ready.once([] {
+            return cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        3 * (kMaxPlanRequests + 1) * (int)sizeof(int32_t));
+        });
         if (e != cudaSuccess) return fail(MOE_ECUDA, "kv_plan: %s", cudaGetErrorString(e));
     }
     const int want = (cap + 1023) / 1024 + (R + 15) / 16;

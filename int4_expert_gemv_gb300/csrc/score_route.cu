@@ -368,23 +368,30 @@ __global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const Route
 }
 
 template <typename X, bool SIGMOID, int LT, int SUB>
-void launch_sub(const RouteParams &p, cudaStream_t st) {
+int launch_sub(const RouteParams &p, cudaStream_t st) {
     constexpr int TOK = kRouteThreads / LT;
     constexpr size_t smem = (size_t)TOK * route_token_floats(LT, SUB) * sizeof(float);
     static_assert(smem <= 200 * 1024, "shared memory of a CTA");
     auto kernel = p.vec ? scored_route_kernel<X, LT, SUB, SIGMOID, true> : scored_route_kernel<X, LT, SUB, SIGMOID, false>;
-    if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) {
+        static OnDevices ready[2];
+        const cudaError_t e = ready[p.vec].once(
+            [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
+        if (e != cudaSuccess) return fail(MOE_ECUDA, "scored_route_kernel: %s", cudaGetErrorString(e));
+    }
     kernel<<<(unsigned)((p.T + TOK - 1) / TOK), kRouteThreads, smem, st>>>(p);
+    return check_launch("scored_route_kernel");
 }
 
 template <typename X, bool SIGMOID, int LT>
-void launch_lt(const RouteParams &p, cudaStream_t st) {
+int launch_lt(const RouteParams &p, cudaStream_t st) {
     const int n = (p.nsub + LT - 1) / LT;             // blocks of a lane: 5 or 20 at most (E <= 1024, 32 groups)
     if (n <= 1) return launch_sub<X, SIGMOID, LT, 1>(p, st);
     if (n <= 2) return launch_sub<X, SIGMOID, LT, 2>(p, st);
     if (n <= 4) return launch_sub<X, SIGMOID, LT, 4>(p, st);
-    if (LT == 32) return launch_sub<X, SIGMOID, LT, 5>(p, st);
-    if constexpr (LT == 8) {
+    if constexpr (LT == 32) {
+        return launch_sub<X, SIGMOID, LT, 5>(p, st);
+    } else {
         if (n <= 8) return launch_sub<X, SIGMOID, LT, 8>(p, st);
         if (n <= 16) return launch_sub<X, SIGMOID, LT, 16>(p, st);
         return launch_sub<X, SIGMOID, LT, 20>(p, st);
@@ -392,13 +399,12 @@ void launch_lt(const RouteParams &p, cudaStream_t st) {
 }
 
 template <typename X, bool SIGMOID>
-void launch_route(const RouteParams &p, cudaStream_t st) {
+int launch_route(const RouteParams &p, cudaStream_t st) {
     // 32 lanes a token while that does not fill the SMs.  Measured, 32 against
     // 8 lanes: 1 x 256 3.7 / 5.7 us, 2525 x 160 5.2 / 5.5, 4096 x 512 5.3 /
     // 6.5, but 4433 x 60 5.4 / 3.2, 9028 x 64 9.1 / 3.8, 65521 x 256 80 / 35.
     const int most = num_sms() * (p.nsub > 16 ? 32 : 8);
-    if (p.T <= most) launch_lt<X, SIGMOID, 32>(p, st);
-    else launch_lt<X, SIGMOID, 8>(p, st);
+    return p.T <= most ? launch_lt<X, SIGMOID, 32>(p, st) : launch_lt<X, SIGMOID, 8>(p, st);
 }
 
 }  // namespace
@@ -457,12 +463,7 @@ extern "C" int moe_scored_route(const moe_route_desc *rd, const void *logits, in
     p.idx = idx;
     p.w = w;
     const bool sig = rd->score == MOE_SCORE_SIGMOID;
-    if (logits_dtype == MOE_DTYPE_F32) {
-        if (sig) launch_route<float, true>(p, stream);
-        else launch_route<float, false>(p, stream);
-    } else {
-        if (sig) launch_route<__nv_bfloat16, true>(p, stream);
-        else launch_route<__nv_bfloat16, false>(p, stream);
-    }
-    return check_launch("scored_route_kernel");
+    if (logits_dtype == MOE_DTYPE_F32)
+        return sig ? launch_route<float, true>(p, stream) : launch_route<float, false>(p, stream);
+    return sig ? launch_route<__nv_bfloat16, true>(p, stream) : launch_route<__nv_bfloat16, false>(p, stream);
 }

@@ -145,22 +145,29 @@ def last_error() -> str:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:       # None or an address
         return t
-    return t.data_ptr()
+
+
+_current = None
 
 
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream() without making a Stream object (2.9 us
         # a call on the GPU's host, against 0.2)
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        global _current
+        if _current is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", None)
+            if raw and device and torch.cuda.is_initialized():
+                _current = lambda: raw(device())  # noqa: E731
+            else:
+                return torch.cuda.current_stream().cuda_stream
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -175,13 +182,18 @@ def _nbytes(t):
     return 0 if t is None else (t.numel() * t.element_size() if not isinstance(t, int) else 0)
 
 
+_dtypes = None
+
+
 def _dtype_code(x) -> int:
-    import torch
-    if x.dtype == torch.float32:
-        return MOE_DTYPE_F32
-    if x.dtype == torch.bfloat16:
-        return MOE_DTYPE_BF16
-    raise TypeError(f"activations must be float32 or bfloat16, got {x.dtype}")
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16}
+    try:
+        return _dtypes[x.dtype]
+    except KeyError:
+        raise TypeError(f"activations must be float32 or bfloat16, got {x.dtype}") from None
 
 
 # ------------------------------------------------------------------ sizes
@@ -288,6 +300,8 @@ def _row_stride(t) -> int:
     """Elements between the rows of a tensor whose rows are contiguous."""
     if t.is_contiguous():
         return t.numel() // max(1, t.shape[0])
+    if t.dim() == 2 and t.stride(1) == 1:
+        return t.stride(0)
     inner = 1
     for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if n != 1 and st != inner:
