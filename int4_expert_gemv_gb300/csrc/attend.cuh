@@ -697,23 +697,26 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     }
 }
 
-// Joins a row's parts, one CTA per (row in several parts, head): warp w takes
-// every JW-th part, its lanes four dimensions each.
-template <bool QF32, int JW>
-__global__ void __launch_bounds__(32 * JW) attend_join_kernel(const AttendParams p, int dp, int rows) {
-    __shared__ float4 acc_s[JW][64];
-    __shared__ float2 ml_s[JW];
+// Joins a row's parts: JW warps for each (row in several parts, head), HB
+// heads a CTA.  Warp w of a head takes every JW-th part, its lanes four
+// dimensions each (and four more past 128).  Many rows have few parts each,
+// and a warp for each head is enough; few rows have many.
+template <bool QF32, int JW, int HB>
+__global__ void __launch_bounds__(32 * JW * HB) attend_join_kernel(const AttendParams p, int dp, int rows) {
+    __shared__ float4 acc_s[JW > 1 ? JW * HB : 1][64];
+    __shared__ float2 ml_s[JW * HB];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 meta = p.meta[blockIdx.x];
-    const int n = meta.x, HT = p.Hkv * p.tiles, r = blockIdx.y;
+    const int n = meta.x, HT = p.Hkv * p.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * HB + warp / JW, w = warp % JW;
     if (n == 0) return;
-    const int b = meta.y / HT, ht = meta.y - b * HT, h = ht / p.tiles, head0 = h * p.G + (ht - h * p.tiles) * rows;
-    if (head0 + r >= (h + 1) * p.G) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = dp / 4;      // float4s of a row: 16 .. 64
+    const int b = meta.y / HT, ht = meta.y - b * HT, h = ht / p.tiles, head = h * p.G + (ht - h * p.tiles) * rows + r;
+    const bool live = r < rows && head < (h + 1) * p.G;
+    const int q = dp / 4;                             // float4s of a row: 16 .. 64
     auto slot = [&](int j) { return (j == 0 ? (size_t)meta.w : 2 * ((size_t)meta.z + j)) * rows + r; };
     float M = -INFINITY, L = 0.0f;
     float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-    for (int j0 = warp; j0 < n; j0 += 32 * JW) {      // 32 parts of this warp: their (m, l), one a lane
+    for (int j0 = w; live && j0 < n; j0 += 32 * JW) { // 32 parts of this warp: their (m, l), one a lane
         const int jl = j0 + JW * lane;
         const float2 ml = jl < n ? p.part_ml[slot(jl)] : make_float2(-INFINITY, 0.0f);
         float top = ml.x;
@@ -741,27 +744,39 @@ __global__ void __launch_bounds__(32 * JW) attend_join_kernel(const AttendParams
             }
         }
     }
-    acc_s[warp][lane] = acc[0];
-    acc_s[warp][lane + 32] = acc[1];
-    if (lane == 0) ml_s[warp] = make_float2(M, L);
-    __syncthreads();
-    if (tid < q && 4 * tid < p.D) {
-        M = -INFINITY;
-        for (int w = 0; w < JW; w++) M = fmaxf(M, ml_s[w].x);
+    if (JW > 1) {                                     // the warps' sums, by the head's first warp
+        acc_s[warp][lane] = acc[0];
+        acc_s[warp][lane + 32] = acc[1];
+        if (lane == 0) ml_s[warp] = make_float2(M, L);
+        __syncthreads();
+        if (w != 0) return;
+        for (int k = 1; k < JW; k++) M = fmaxf(M, ml_s[warp + k].x);
         const float ref = M == -INFINITY ? 0.0f : M;
-        float4 a = make_float4(0, 0, 0, 0);
+        acc[0] = acc[1] = make_float4(0, 0, 0, 0);
         L = 0.0f;
-        for (int w = 0; w < JW; w++) {
-            const float f = exp2_f(ml_s[w].x - ref);
-            const float4 e = acc_s[w][tid];
-            a.x = fmaf(f, e.x, a.x), a.y = fmaf(f, e.y, a.y), a.z = fmaf(f, e.z, a.z), a.w = fmaf(f, e.w, a.w);
-            L = fmaf(f, ml_s[w].y, L);
+        for (int k = 0; k < JW; k++) {
+            const float f = exp2_f(ml_s[warp + k].x - ref);
+            L = fmaf(f, ml_s[warp + k].y, L);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const float4 e = acc_s[warp + k][lane + 32 * c];
+                acc[c].x = fmaf(f, e.x, acc[c].x);
+                acc[c].y = fmaf(f, e.y, acc[c].y);
+                acc[c].z = fmaf(f, e.z, acc[c].z);
+                acc[c].w = fmaf(f, e.w, acc[c].w);
+            }
         }
-        const float inv = (p.v_scale ? p.v_scale[h] : 1.0f) / L;
-        store4<QF32>(p.out, (size_t)b * p.out_stride + (size_t)(head0 + r) * p.D + 4 * tid,
-                     make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
-        if (tid == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + r] = 0.69314718055994531f * (M + log2f(L));
     }
+    if (!live) return;
+    const float inv = (p.v_scale ? p.v_scale[h] : 1.0f) / L;
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        const int d = 4 * (lane + 32 * c);
+        if (d < p.D)
+            store4<QF32>(p.out, (size_t)b * p.out_stride + (size_t)head * p.D + d,
+                         make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
+    }
+    if (lane == 0 && p.lse) p.lse[(size_t)b * p.Hq + head] = 0.69314718055994531f * (M + log2f(L));
 }
 
 // ---------------------------------------------------------------- launch
@@ -788,19 +803,20 @@ int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     }
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_kernel: %s", cudaGetErrorString(e));
     if (p.whole) return MOE_OK;
-    // few rows: many parts each, so many warps; else a small CTA that mostly finds nothing to do
-    const bool few = rows * 8 <= p.ctas;
+    const int64_t parts = p.ctas / rows;              // of a row, when the lengths are alike
+    const int heads = min(S::ROWS, p.G), hb = parts > 32 ? 1 : parts > 4 ? 2 : 8;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.by_row ? rows : p.ctas), (unsigned)min(S::ROWS, p.G));
-    cfg.blockDim = dim3(few ? 512 : 256);
+    cfg.gridDim = dim3((unsigned)(p.by_row ? rows : p.ctas), (unsigned)((heads + hb - 1) / hb));
+    cfg.blockDim = dim3(parts > 32 ? 512 : 256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = few ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 16>, p, DP, (int)S::ROWS)
-            : cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 8>, p, DP, (int)S::ROWS);
+    e = parts > 32  ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 16, 1>, p, DP, (int)S::ROWS)
+        : parts > 4 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 4, 2>, p, DP, (int)S::ROWS)
+                    : cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 1, 8>, p, DP, (int)S::ROWS);
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_join_kernel: %s", cudaGetErrorString(e));
     return MOE_OK;
 }
