@@ -22,9 +22,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
-
 struct PlanParams {
     const int32_t *seq, *add;
     int R;
@@ -56,63 +53,87 @@ __device__ __forceinline__ int owner(const int32_t *sum, int R, int i) {
 
 __device__ __forceinline__ int wrap(int64_t i, int n) { return (int)(i < n ? i : i - n); }
 
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams p) {
+// Sums that stick at 2^32 - 1, far above any that fits.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < b ? 0xffffffffu : s;
+}
+
+__device__ __forceinline__ uint32_t scan_sat(uint32_t v, int lane) {       // inclusive, over a warp
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = add_sat(v, u);
+    }
+    return v;
+}
+
+// A thread's items: single tokens, or four neighbours where there are many.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanParams p) {
+    constexpr int WARPS = THREADS / 32;
     extern __shared__ int32_t sums[];               // [3][R + 1]
-    __shared__ int64_t part[3][kPlanWarps];
+    __shared__ uint32_t part[4][32];                // the warps' sums and flags
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.R;
-    int32_t *s_new = sums, *s_need = sums + R + 1, *s_gone = sums + 2 * (R + 1);
+    const int32_t *s_new = sums, *s_need = sums + R + 1, *s_gone = sums + 2 * (R + 1);
     const int page = p.page.d;
     const int head = p.pool[0], n_free = p.pool[1];
     const int64_t room = (int64_t)p.max_blocks * page;
 
     // this thread's run of requests
-    const int run = (R + kPlanThreads - 1) / kPlanThreads;
+    const int run = (R + THREADS - 1) / THREADS;
     const int r0 = min(R, tid * run), r1 = min(R, r0 + run);
     bool invalid = head < 0 || head >= p.n_pages || n_free < 0 || n_free > p.n_pages;
     bool nospace = false;
-    int64_t sum[3] = {0, 0, 0};
+    uint32_t sum[3] = {0, 0, 0};
+#pragma unroll 4
     for (int r = r0; r < r1; r++) {
-        const int len = p.seq[r], add = p.add[r];
+        const int len = __ldg(p.seq + r), add = __ldg(p.add + r);
         if (len < 0 || len > room || add < -1) {
             invalid = true;
             continue;
         }
         const int have = p.page.ceil(len);
+        int item[3] = {0, 0, 0};                    // kept where their sums will stand
         if (add < 0) {
-            sum[2] += have;
+            item[2] = have;
         } else if ((int64_t)len + add > room || (int64_t)len + add > INT32_MAX) {
             nospace = true;
         } else {
-            sum[0] += add;
-            sum[1] += p.page.ceil(len + add) - have;
+            item[0] = add;
+            item[1] = p.page.ceil(len + add) - have;
         }
+#pragma unroll
+        for (int j = 0; j < 3; j++) {
+            sum[j] = add_sat(sum[j], item[j]);
+            sums[j * (R + 1) + r] = item[j];
+        }
+        if (blockIdx.x == 0) p.seq_out[r] = add < 0 ? 0 : len + item[0];
     }
-    int64_t upto[3];
+    uint32_t upto[3], total[3];
 #pragma unroll
     for (int j = 0; j < 3; j++) {
-        int64_t v = sum[j];
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        upto[j] = v - sum[j];
-        if (lane == 31) part[j][warp] = v;
+        upto[j] = scan_sat(sum[j], lane);
+        if (lane == 31) part[j][warp] = upto[j];
     }
+    invalid = __any_sync(0xffffffffu, invalid);
+    nospace = __any_sync(0xffffffffu, nospace);
+    if (lane == 0) part[3][warp] = (invalid ? 1u : 0u) | (nospace ? 2u : 0u);
     __syncthreads();
-    int64_t total[3] = {0, 0, 0};
+    const uint32_t flags = __reduce_or_sync(0xffffffffu, lane < WARPS ? part[3][lane] : 0u);
 #pragma unroll
-    for (int j = 0; j < 3; j++)
-        for (int w = 0; w < kPlanWarps; w++) {
-            if (w == warp) upto[j] += total[j];
-            total[j] += part[j][w];
-        }
-    nospace |= total[0] > p.cap || total[1] > n_free;
+    for (int j = 0; j < 3; j++) {
+        const uint32_t v = scan_sat(lane < WARPS ? part[j][lane] : 0u, lane);
+        total[j] = __shfl_sync(0xffffffffu, v, 31);
+        const uint32_t before = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
+        upto[j] = upto[j] - sum[j] + (warp > 0 ? before : 0u);      // exact unless a total sticks, which is refused
+    }
     // more pages held than there are: the tables and the ring contradict each other
-    invalid |= n_free + total[2] > p.n_pages;
-    const int bad_i = __syncthreads_or(invalid), bad_s = __syncthreads_or(nospace);
-    const int step = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;
-    if (bad_i || bad_s) {                           // the same answer in every CTA
-        for (int r = me; r < R; r += step) p.seq_out[r] = p.seq[r];
+    invalid = (flags & 1u) || (uint64_t)n_free + total[2] > (uint64_t)p.n_pages;
+    nospace = (flags & 2u) || total[0] > (uint32_t)p.cap || total[1] > (uint32_t)n_free;
+    const int step = gridDim.x * THREADS, me = blockIdx.x * THREADS + tid;
+    if (invalid || nospace) {                       // the same answer in every CTA
+        if (blockIdx.x == 0)                        // (where this CTA has written its sums)
+            for (int r = r0; r < r1; r++) p.seq_out[r] = p.seq[r];
         for (int r = me; r <= R; r += step) p.first[r] = 0;
         for (int i = me; i < p.cap; i += step) {
             p.slots[i] = -1;
@@ -121,25 +142,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         if (me == 0) {
             p.pool_out[0] = head;
             p.pool_out[1] = n_free;
-            p.status[0] = bad_i ? MOE_EINVAL : MOE_ENOSPACE;
+            p.status[0] = invalid ? MOE_EINVAL : MOE_ENOSPACE;
         }
         return;
     }
     for (int r = r0; r < r1; r++) {
-        const int len = p.seq[r], add = p.add[r];
-        const int have = p.page.ceil(len);
-        s_new[r] = (int)upto[0];
-        s_need[r] = (int)upto[1];
-        s_gone[r] = (int)upto[2];
-        if (blockIdx.x == 0) {
-            p.first[r] = (int)upto[0];
-            p.seq_out[r] = add < 0 ? 0 : len + add;
-        }
-        if (add < 0) {
-            upto[2] += have;
-        } else {
-            upto[0] += add;
-            upto[1] += p.page.ceil(len + add) - have;
+        if (blockIdx.x == 0) p.first[r] = (int)upto[0];
+#pragma unroll
+        for (int j = 0; j < 3; j++) {
+            const int item = sums[j * (R + 1) + r];
+            sums[j * (R + 1) + r] = (int)upto[j];
+            upto[j] += item;
         }
     }
     const int n_new = (int)total[0], n_need = (int)total[1], n_gone = (int)total[2];
@@ -150,36 +163,41 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         p.status[0] = MOE_OK;
     }
     __syncthreads();
-    // new blocks
-    for (int j = me; j < n_need; j += step) {
-        const int r = owner(s_need, R, j);
-        const int b = p.page.ceil(p.seq[r]) + j - s_need[r];
-        p.table[(size_t)r * p.max_blocks + b] = p.ring[wrap((int64_t)head + j, p.n_pages)];
-    }
-    // returned pages: behind the free part, where no page is being taken
-    for (int j = me; j < n_gone; j += step) {
-        const int r = owner(s_gone, R, j);
-        p.ring[(int)(((int64_t)head + n_free + j) % p.n_pages)] =
-            p.table[(size_t)r * p.max_blocks + j - s_gone[r]];
-    }
-    // slots and places, four neighbours a thread: one search for the first, and
-    // a new length, block or page only where it changes
-    const bool vec = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.places)) & 15) == 0;
-    for (int64_t i0 = 4 * (int64_t)me; i0 < p.cap; i0 += 4 * (int64_t)step) {
+
+    // The items of all three kinds in one run, so that their chains of loads
+    // overlap: slots and places, new blocks, returned pages.
+    const int four = p.cap > step ? 4 : 1;
+    const int64_t n_item = ((int64_t)p.cap + four - 1) / four, all = n_item + n_need + n_gone;
+    const bool vec = four == 4 && ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.places)) & 15) == 0;
+    for (int64_t it = me; it < all; it += step) {
+        if (it >= n_item + n_need) {                // behind the ring's free part, where no page is being taken
+            const int j = (int)(it - n_item - n_need), r = owner(s_gone, R, j);
+            p.ring[wrap((int64_t)head + n_free + j, p.n_pages)] = p.table[(size_t)r * p.max_blocks + j - s_gone[r]];
+            continue;
+        }
+        if (it >= n_item) {
+            const int j = (int)(it - n_item), r = owner(s_need, R, j);
+            const int b = p.page.ceil(__ldg(p.seq + r)) + j - s_need[r];
+            p.table[(size_t)r * p.max_blocks + b] = p.ring[wrap((int64_t)head + j, p.n_pages)];
+            continue;
+        }
+        // one search for the first token, and a new length, block or page
+        // only where it changes
+        const int64_t i0 = it * four;
         int slot[4] = {-1, -1, -1, -1}, place[4] = {0, 0, 0, 0};
         if (i0 < n_new) {
             int r = owner(s_new, R, (int)i0), next = r + 1 < R ? s_new[r + 1] : n_new;
-            int len = p.seq[r], have = p.page.ceil(len), blk = -1, id = -1;
+            int len = __ldg(p.seq + r), have = p.page.ceil(len), blk = -1, id = -1;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const int i = (int)i0 + j;
-                if (i >= n_new) break;
+                if (j >= four || i >= n_new) break;
                 if (i >= next) {
                     do {
                         r++;
                         next = r + 1 < R ? s_new[r + 1] : n_new;
                     } while (i >= next);
-                    len = p.seq[r];
+                    len = __ldg(p.seq + r);
                     have = p.page.ceil(len);
                     blk = -1;
                 }
@@ -197,12 +215,29 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
             *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
             *reinterpret_cast<int4 *>(p.places + i0) = make_int4(place[0], place[1], place[2], place[3]);
         } else {
-            for (int j = 0; j < 4 && i0 + j < p.cap; j++) {
+            for (int j = 0; j < four && i0 + j < p.cap; j++) {
                 p.slots[i0 + j] = slot[j];
                 p.places[i0 + j] = place[j];
             }
         }
     }
+}
+
+template <int THREADS>
+int launch_plan(const PlanParams &p, cudaStream_t st) {
+    const size_t smem = 3 * (size_t)(p.R + 1) * sizeof(int32_t);
+    if (smem > 48 * 1024) {
+        static OnDevices ready;
+        const cudaError_t e = ready.once([] {
+            return cudaFuncSetAttribute(kv_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        3 * (kMaxPlanRequests + 1) * (int)sizeof(int32_t));
+        });
+        if (e != cudaSuccess) return fail(MOE_ECUDA, "kv_plan: %s", cudaGetErrorString(e));
+    }
+    const int64_t want = ((int64_t)p.cap + 2047) / 2048 + (p.R + 15) / 16;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, num_sms()));
+    kv_plan_kernel<THREADS><<<grid, THREADS, smem, st>>>(p);
+    return check_launch("kv_plan_kernel");
 }
 
 // ---------------------------------------------------------------- append
@@ -340,18 +375,7 @@ extern "C" int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R
         return fail(MOE_EINVAL, "kv_plan: an output is an input");
     const PlanParams p{seq_len, new_len, R, block_table, max_blocks, FastDiv(page), ring, n_pages,
                        pool, seq_out, first, slots, places, cap, pool_out, status};
-    const size_t smem = 3 * (size_t)(R + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        static OnDevices ready;
-        const cudaError_t e = ready.once([] {
-            return cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        3 * (kMaxPlanRequests + 1) * (int)sizeof(int32_t));
-        });
-        if (e != cudaSuccess) return fail(MOE_ECUDA, "kv_plan: %s", cudaGetErrorString(e));
-    }
-    const int want = (cap + 1023) / 1024 + (R + 15) / 16;
-    kv_plan_kernel<<<std::max(1, std::min(want, num_sms())), kPlanThreads, smem, stream>>>(p);
-    return check_launch("kv_plan_kernel");
+    return R > 1024 ? launch_plan<1024>(p, stream) : launch_plan<512>(p, stream);
 }
 
 extern "C" int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const void *v,
