@@ -157,9 +157,11 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
     return r;
 }
 
-template <int DP, bool F8, bool QF32, bool FULL>
+// SOLO: every warp takes rows of its own, whole ones, and no barrier joins it
+// to the others.
+template <int DP, bool F8, bool QF32, bool FULL, bool SOLO>
 struct AttendShape {
-    static constexpr int NW = kAttWarps;
+    static constexpr int NW = SOLO ? 1 : kAttWarps;           // warps that share a row
     static constexpr int ELT = F8 ? 1 : 2;
     static constexpr int CH = DP * ELT / 16;                  // 16-byte chunks of a row
     static constexpr int NQ = QF32 ? (F8 ? 2 : 3) : 1;        // parts of q
@@ -176,15 +178,17 @@ struct AttendShape {
     // three CTAs of two stages beat two of three (29 windows of 1000: 39
     // against 44 us; 64 ragged bf16 requests: 153 against 152).
     static constexpr bool BUSY = QF32 && !FULL;
-    static constexpr int NS = F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3) : (DP == 128 ? (BUSY ? 2 : 3) : DP == 256 ? 3 : 4);
+    static constexpr int NS = SOLO ? 2
+                              : F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3)
+                                   : (DP == 128 ? (BUSY ? 2 : 3) : DP == 256 ? 3 : 4);
     static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP == 64 ? 3 : DP == 128 ? (BUSY ? 3 : 2) : 1);
-    static constexpr int THREADS = 32 * NW, UNIT = kAttTile * NW;
+    static constexpr int UNIT = kAttTile * NW;
     static constexpr int RING = NS * STAGE;                   // of one warp
     static constexpr bool HALF = !FULL && NQ == 1;            // operand rows 8-15 of q are zero and not stored
     static constexpr int Q_B = NA * STEPS * (HALF ? 256 : 512);
     static constexpr int LDO = DP + 4;                        // floats of a row of O in the join of the warps
-    static constexpr int SMEM = NW * RING + Q_B;
-    static_assert(ROWS * LDO * 4 <= RING, "a warp's O fits its ring");
+    static constexpr int SMEM = kAttWarps * RING + kAttWarps / NW * Q_B;
+    static_assert(SOLO || ROWS * LDO * 4 <= RING, "a warp's O fits its ring");
 };
 
 // Chunk c of row r of a tile: keys are read by 8 rows x 4 neighbouring
@@ -225,24 +229,29 @@ __device__ __forceinline__ void store4(void *out, size_t i, float4 f) {
 }
 
 // ---------------------------------------------------------------- kernel
-template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FULL>::CTAS))
+template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED, bool SOLO>
+__global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FULL, SOLO>::CTAS))
     attend_kernel(const AttendParams p) {
-    using S = AttendShape<DP, F8, QF32, FULL>;
-    constexpr int NW = S::NW, CH = S::CH, NS = S::NS, ROWS = S::ROWS, R = FULL ? 2 : 1, THREADS = S::THREADS, UNIT = S::UNIT;
+    using S = AttendShape<DP, F8, QF32, FULL, SOLO>;
+    constexpr int NW = S::NW, CH = S::CH, NS = S::NS, ROWS = S::ROWS, R = FULL ? 2 : 1, UNIT = S::UNIT;
+    constexpr int THREADS = 32 * kAttWarps, TEAMS = kAttWarps / NW;       // a team: the warps of a row
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sm_sum[NW];
-    __shared__ int64_t sm_off;
-    __shared__ int sm_b, sm_bad;
-    __shared__ float sm_c[16];
-    __shared__ float2 sm_ml[NW][16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int cta = blockIdx.x, HT = p.Hkv * p.tiles;
+    __shared__ int64_t sm_sum[kAttWarps];
+    __shared__ int64_t sm_off[TEAMS];
+    __shared__ int sm_b[TEAMS], sm_bad;
+    __shared__ float sm_c[TEAMS][16];
+    __shared__ float2 sm_ml[kAttWarps][16];
+    const int tid = threadIdx.x, lane = tid & 31, wrp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int team = wrp / NW, warp = wrp % NW, cta = blockIdx.x * TEAMS + team, HT = p.Hkv * p.tiles;
+    auto sync = [] {
+        if (SOLO) __syncwarp();
+        else __syncthreads();
+    };
     const int room = (int)min((int64_t)p.max_blocks * p.page.d, (int64_t)kMaxLength);
     asm volatile("griddepcontrol.launch_dependents;");   // the join may take the SMs as they empty
-    uint8_t *ring = smem + warp * S::RING;
+    uint8_t *ring = smem + wrp * S::RING;
     const uint32_t ring_a = smem_addr(ring);
-    uint8_t *q_s = smem + NW * S::RING;
+    uint8_t *q_s = smem + kAttWarps * S::RING + team * S::Q_B;
 
     // where this CTA's run begins
     const int run = (p.B + THREADS - 1) / THREADS;
@@ -254,40 +263,44 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         const int64_t u = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += u;
     }
-    if (lane == 31) sm_sum[warp] = before;
+    if (lane == 31) sm_sum[wrp] = before;
     before -= sum;
-    for (int i = tid; i < S::Q_B / 16; i += THREADS) reinterpret_cast<uint4 *>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < TEAMS * S::Q_B / 16; i += THREADS)
+        reinterpret_cast<uint4 *>(smem + kAttWarps * S::RING)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     int64_t W = 0;
 #pragma unroll
-    for (int w = 0; w < NW; w++) {
-        if (w == warp) before += W;
+    for (int w = 0; w < kAttWarps; w++) {
+        if (w == wrp) before += W;
         W += sm_sum[w];
     }
     W *= HT;
-    // a unit for each CTA while that makes at most 64 parts of a row, then four
-    const int n_cta = (int)min((int64_t)p.ctas, max(W / 4, min(W, (int64_t)p.B * HT * 64)));
+    // a unit for each team while that makes at most 64 parts of a row, then four
+    const int n_cta = (int)min((int64_t)p.ctas * TEAMS, max(W / 4, min(W, (int64_t)p.B * HT * 64)));
     if (tid == 0 && !p.by_row && !p.whole) p.meta[cta] = make_int4(0, 0, 0, 0);
-    int64_t u0 = 0, u1 = 0;
-    if (cta < n_cta) {
-        u0 = cta * W / n_cta;
-        u1 = (cta + 1) * W / n_cta;
-        if (u0 >= before * HT && u0 < (before + sum) * HT) {
+#pragma unroll
+    for (int k = 0; k < TEAMS; k++) {          // a thread in whose requests a team's run begins says so
+        const int c = blockIdx.x * TEAMS + k;
+        if (c >= n_cta) continue;
+        const int64_t u = c * W / n_cta;
+        if (u >= before * HT && u < (before + sum) * HT) {
             int64_t at = before;
             int b = b0;
             for (;; b++) {
                 const int n = units_of<UNIT>(p.seq[b], p.window, room);
-                if (u0 < (at + n) * HT) break;
+                if (u < (at + n) * HT) break;
                 at += n;
             }
-            sm_b = b;
-            sm_off = u0 - at * HT;
+            sm_b[k] = b;
+            sm_off[k] = u - at * HT;
         }
     }
     __syncthreads();
 
-    int b = cta < n_cta ? sm_b : 0;
-    int64_t off = cta < n_cta ? sm_off : 0;
+    const bool busy = cta < n_cta;
+    const int64_t u0 = busy ? cta * W / n_cta : 0, u1 = busy ? (cta + 1) * W / n_cta : 0;
+    int b = busy ? sm_b[team] : 0;
+    int64_t off = busy ? sm_off[team] : 0;
     bool first_seg = true;
     for (int64_t u = u0; u < u1;) {
         const int full_len = p.seq[b];
@@ -312,7 +325,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         const int stop = min(len, tile0 + n_unit * UNIT);
         const int n_tile = (stop - tile0 + kAttTile - 1) / kAttTile;
         const int mine = n_tile > warp ? (n_tile - warp + NW - 1) / NW : 0;
-        if (tid == 0) sm_bad = full_len > room;
+        if (!SOLO && tid == 0) sm_bad = full_len > room;
 
         // ---- q: the numbers are loaded before the first tiles are asked for, and split after
         constexpr int QR = ROWS / NW, IT = (DP / 4 + 31) / 32;
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                     c *= __uint_as_float((uint32_t)max(1, e - 13) << 23);
                 }
             }
-            if (lane == 0) sm_c[r] = c;
+            if (lane == 0) sm_c[team][r] = c;
 #pragma unroll
             for (int i = 0; i < IT; i++) {
                 const int d = 4 * (lane + 32 * i);
@@ -445,11 +458,11 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                 }
             }
         }
-        __syncthreads();
+        sync();
         float c[R], m[R], l[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            c[r] = sm_c[g + 8 * r];
+            c[r] = sm_c[team][g + 8 * r];
             m[r] = -INFINITY;
             l[r] = 0.0f;
         }
@@ -613,6 +626,40 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         copy_wait<0>();
         __syncwarp();
 
+        const float v_scale = F8 && p.v_scale ? p.v_scale[h] : 1.0f;
+        if (SOLO) {                     // ---- the warp's row, out of its registers
+            bad = __any_sync(0xffffffffu, bad) || full_len > room;
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (bad) l[r] = NAN;
+                const int row = g + 8 * r;
+                if (row >= n_rows) continue;
+                const float inv = v_scale / l[r];
+                const size_t at = (size_t)b * p.out_stride + (size_t)(head0 + row) * p.D;
+#pragma unroll
+                for (int un = 0; un < DP / 64; un++)
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        const int d = un * 64 + 16 * t + 8 * hf;
+                        if (d >= p.D) continue;
+                        float w[8];
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const float *e = o[un * 8 + j];
+                            w[j] = (FULL ? e[2 * r + hf] : e[hf] + e[2 + hf]) * inv;
+                        }
+                        store4<QF32>(p.out, at + d, make_float4(w[0], w[1], w[2], w[3]));
+                        store4<QF32>(p.out, at + d + 4, make_float4(w[4], w[5], w[6], w[7]));
+                    }
+                if (t == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + row] = 0.69314718055994531f * (m[r] + log2f(l[r]));
+            }
+            __syncwarp();
+            u += n_unit;
+            off += n_unit;
+            continue;
+        }
         // ---- the warps' parts of the row
         if (bad) sm_bad = 1;
         float *o_s = reinterpret_cast<float *>(ring);
@@ -639,7 +686,6 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         }
         __syncthreads();
         const bool whole = n_unit == nb;
-        const float v_scale = F8 && p.v_scale ? p.v_scale[h] : 1.0f;
         const int slot = 2 * cta + (first_seg ? 0 : 1);
         for (int i = tid; i < n_rows * (DP / 4); i += THREADS) {
             const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
@@ -686,7 +732,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     }
 
     // rows with nothing to see
-    for (int e = cta; e < p.B; e += gridDim.x) {
+    for (int e = blockIdx.x; e < p.B; e += gridDim.x) {
         if (units_of<UNIT>(p.seq[e], p.window, room) > 0) continue;
         for (int i = tid; i < p.Hq * p.D / 4; i += THREADS)
             store4<QF32>(p.out, (size_t)e * p.out_stride + 4 * (size_t)i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
@@ -780,29 +826,44 @@ __global__ void __launch_bounds__(32 * JW * HB) attend_join_kernel(const AttendP
 }
 
 // ---------------------------------------------------------------- launch
-template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
-int launch_attend_kernel(AttendParams p, cudaStream_t st) {
-    using S = AttendShape<DP, F8, QF32, FULL>;
-    auto kernel = attend_kernel<DP, F8, QF32, FULL, ALIGNED>;
-    p.ctas = num_sms() * S::CTAS;
-    const int64_t rows = (int64_t)p.B * p.Hkv * p.tiles;
-    p.by_row = rows <= p.ctas;
-    // Rows of at most four units (by the table's width and the window) are
-    // not cut: a CTA takes those that begin in its run, which costs less than
-    // the join and its launch.
-    const int64_t room = (int64_t)p.max_blocks * p.page.d;
-    const int64_t longest = p.window > 0 && p.window + kAttTile < room ? p.window + kAttTile : room;
-    p.whole = longest <= 4 * S::UNIT;
+template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED, bool SOLO>
+int launch_attend_rows(const AttendParams &p, cudaStream_t st) {
+    using S = AttendShape<DP, F8, QF32, FULL, SOLO>;
+    auto kernel = attend_kernel<DP, F8, QF32, FULL, ALIGNED, SOLO>;
     static OnDevices ready;
     cudaError_t e = ready.once([&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     });
     if (e == cudaSuccess) {
-        kernel<<<p.ctas, S::THREADS, S::SMEM, st>>>(p);
+        kernel<<<p.ctas, 32 * kAttWarps, S::SMEM, st>>>(p);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_kernel: %s", cudaGetErrorString(e));
-    if (p.whole) return MOE_OK;
+    return MOE_OK;
+}
+
+template <int DP, bool F8, bool QF32, bool FULL, bool ALIGNED>
+int launch_attend_kernel(AttendParams p, cudaStream_t st) {
+    using S = AttendShape<DP, F8, QF32, FULL, false>;
+    p.ctas = num_sms() * S::CTAS;
+    const int64_t rows = (int64_t)p.B * p.Hkv * p.tiles;
+    p.by_row = rows <= p.ctas;
+    // Rows of at most four units (by the table's width and the window) are
+    // not cut: a CTA takes those that begin in its run, which costs less than
+    // the join and its launch.  Where there are many, each warp takes rows of
+    // its own: a row costs about as much as four tiles of it before its first
+    // product, which is then paid for four rows at once.
+    const int64_t room = (int64_t)p.max_blocks * p.page.d;
+    const int64_t longest = p.window > 0 && p.window + kAttTile < room ? p.window + kAttTile : room;
+    p.whole = longest <= 4 * S::UNIT;
+    if (p.whole) {
+        const int64_t tile = (longest + kAttTile - 1) / kAttTile;
+        const int64_t shared = (rows + p.ctas - 1) / p.ctas * (4 + (tile + 3) / 4);
+        const int64_t solo = (rows + 4 * p.ctas - 1) / (4 * p.ctas) * (4 + tile);
+        return solo < shared ? launch_attend_rows<DP, F8, QF32, FULL, ALIGNED, true>(p, st)
+                             : launch_attend_rows<DP, F8, QF32, FULL, ALIGNED, false>(p, st);
+    }
+    if (int rc = launch_attend_rows<DP, F8, QF32, FULL, ALIGNED, false>(p, st)) return rc;
     const int64_t parts = p.ctas / rows;              // of a row, when the lengths are alike
     const int heads = min(S::ROWS, p.G), hb = parts > 32 ? 1 : parts > 4 ? 2 : 8;
     cudaLaunchConfig_t cfg{};
@@ -814,7 +875,8 @@ int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = parts > 32  ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 16, 1>, p, DP, (int)S::ROWS)
+    const cudaError_t e =
+        parts > 32  ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 16, 1>, p, DP, (int)S::ROWS)
         : parts > 4 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 4, 2>, p, DP, (int)S::ROWS)
                     : cudaLaunchKernelEx(&cfg, attend_join_kernel<QF32, 1, 8>, p, DP, (int)S::ROWS);
     if (e != cudaSuccess) return fail(MOE_ECUDA, "attend_join_kernel: %s", cudaGetErrorString(e));
