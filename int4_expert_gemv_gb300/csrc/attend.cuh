@@ -170,8 +170,9 @@ struct AttendShape {
     static constexpr int NA = FULL ? NQ : (NQ + 1) / 2;       // operand tiles of q
     static constexpr int NB = FULL ? NP : (NP + 1) / 2;       // of the weights
     static constexpr int STEPS = DP / 16;
-    static constexpr int TILE_B = kAttTile * DP * ELT;        // bytes of a tile's keys (or values)
-    static constexpr int STAGE = 2 * TILE_B;
+    static constexpr int TILE_B = kAttTile * DP * ELT;        // bytes of a tile's keys
+    static constexpr int STAGE = TILE_B + (CH == 12 ? kAttTile * 13 * 16 : TILE_B);
+    static constexpr bool HALF_UNIT = DP % 64 != 0;           // the last 32 dimensions are half a unit of values
     // Stages and CTAs per SM, of the shared memory (192 KB of stages) and the
     // registers.  More CTAs hide a tile's own latencies better, more stages
     // the memory's: with an fp32 q in up to 8 rows (more products a tile)
@@ -180,8 +181,8 @@ struct AttendShape {
     static constexpr bool BUSY = QF32 && !FULL;
     static constexpr int NS = SOLO ? 2
                               : F8 ? (DP == 64 ? 8 : DP == 128 ? 4 : 3)
-                                   : (DP == 128 ? (BUSY ? 2 : 3) : DP == 256 ? 3 : 4);
-    static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP == 64 ? 3 : DP == 128 ? (BUSY ? 3 : 2) : 1);
+                                   : (DP == 96 || DP == 128 ? (BUSY ? 2 : 3) : DP == 256 ? 3 : 4);
+    static constexpr int CTAS = F8 ? (DP == 256 ? 2 : 3) : (DP == 64 ? 3 : DP <= 128 ? (BUSY ? 3 : 2) : 1);
     static constexpr int UNIT = kAttTile * NW;
     static constexpr int RING = NS * STAGE;                   // of one warp
     static constexpr bool HALF = !FULL && NQ == 1;            // operand rows 8-15 of q are zero and not stored
@@ -195,11 +196,12 @@ struct AttendShape {
 // chunks, values by rows 2t x 8-byte or 16-byte chunks g.
 template <int CH>
 __device__ __forceinline__ uint32_t key_at(int r, int c) {
-    return CH >= 8 ? (uint32_t)(r * CH + (c ^ ((r & 1) << 2))) * 16 : (uint32_t)(r * CH + c) * 16;
+    return CH % 8 == 0 ? (uint32_t)(r * CH + (c ^ ((r & 1) << 2))) * 16 : (uint32_t)(r * CH + c) * 16;
 }
 template <int CH>
 __device__ __forceinline__ uint32_t value_at(int r, int c) {
-    if (CH >= 8) return (uint32_t)(r * CH + (c ^ (r & 6))) * 16;
+    if (CH % 8 == 0) return (uint32_t)(r * CH + (c ^ (r & 6))) * 16;
+    if (CH == 12) return (uint32_t)(r * 13 + c) * 16;         // an odd stride does the same
     const int pos = (r >> 1) | (r & 1) << 3;                  // rows of 64 bytes: even rows first
     return (uint32_t)(pos * CH + (c ^ (pos & 2))) * 16;
 }
@@ -622,6 +624,24 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                     for (int nb2 = 0; nb2 < S::NB; nb2++)
                         mma<F8>(o[un * 8 + j], a[nb2][0], a[nb2][1], a[nb2][2], a[nb2][3], v[0][j], v[1][j]);
             }
+            if (S::HALF_UNIT) {                     // 4 numbers a lane: tile i's column g is dimension 4 g + i of these 32
+                uint32_t v[2][4];
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const int ch = DP / 64 * 8 + (g >> 1), in = (g & 1) * 8;
+                    const uint2 e = lds8(vs + value_at<CH>(2 * t + 8 * hf, ch) + in);
+                    const uint2 d = lds8(vs + value_at<CH>(2 * t + 1 + 8 * hf, ch) + in);
+                    v[hf][0] = __byte_perm(e.x, d.x, 0x5410);
+                    v[hf][1] = __byte_perm(e.x, d.x, 0x7632);
+                    v[hf][2] = __byte_perm(e.y, d.y, 0x5410);
+                    v[hf][3] = __byte_perm(e.y, d.y, 0x7632);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int nb2 = 0; nb2 < S::NB; nb2++)
+                        mma<F8>(o[DP / 64 * 8 + j], a[nb2][0], a[nb2][1], a[nb2][2], a[nb2][3], v[0][j], v[1][j]);
+            }
         }
         copy_wait<0>();
         __syncwarp();
@@ -653,6 +673,20 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                         store4<QF32>(p.out, at + d, make_float4(w[0], w[1], w[2], w[3]));
                         store4<QF32>(p.out, at + d + 4, make_float4(w[4], w[5], w[6], w[7]));
                     }
+                if (S::HALF_UNIT) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        const int d = DP / 64 * 64 + 8 * t + 4 * hf;
+                        if (d >= p.D) continue;
+                        float w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float *e = o[DP / 64 * 8 + j];
+                            w[j] = (FULL ? e[2 * r + hf] : e[hf] + e[2 + hf]) * inv;
+                        }
+                        store4<QF32>(p.out, at + d, make_float4(w[0], w[1], w[2], w[3]));
+                    }
+                }
                 if (t == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + row] = 0.69314718055994531f * (m[r] + log2f(l[r]));
             }
             __syncwarp();
@@ -683,6 +717,19 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                         }
                         *reinterpret_cast<float4 *>(o_s + (g + 8 * r) * S::LDO + un * 64 + 16 * t + 8 * hf + 4 * q4) = w;
                     }
+            if (S::HALF_UNIT) {
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    float4 w;
+                    float *wf = &w.x;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float *e = o[DP / 64 * 8 + j];
+                        wf[j] = FULL ? e[2 * r + hf] : e[hf] + e[2 + hf];
+                    }
+                    *reinterpret_cast<float4 *>(o_s + (g + 8 * r) * S::LDO + DP / 64 * 64 + 8 * t + 4 * hf) = w;
+                }
+            }
         }
         __syncthreads();
         const bool whole = n_unit == nb;
@@ -889,7 +936,7 @@ struct AttendPlan {
 };
 inline AttendPlan attend_plan(int D, bool f8, int G) {
     AttendPlan a;
-    a.dp = D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 && !f8 ? 192 : 256;
+    a.dp = D <= 64 ? 64 : D <= 96 && !f8 ? 96 : D <= 128 ? 128 : D <= 192 && !f8 ? 192 : 256;
     a.rows = G > 8 ? 16 : 8;
     a.ctas_per_sm = f8 ? (a.dp == 256 ? 2 : 3) : (a.dp <= 128 ? 3 : 1);
     return a;

@@ -6,6 +6,7 @@ namespace moe {
 
 int launch_attend_bf16_qf32(const AttendParams &p, int dp, cudaStream_t st) {
     if (dp == 64) return launch_attend_dp<false, true, 64>(p, st);
+    if (dp == 96) return launch_attend_dp<false, true, 96>(p, st);
     if (dp == 128) return launch_attend_dp<false, true, 128>(p, st);
     if (dp == 192) return launch_attend_dp<false, true, 192>(p, st);
     return launch_attend_dp<false, true, 256>(p, st);
