@@ -47,6 +47,8 @@ extern "C" int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_d
                     window);
     if (q_dtype != MOE_DTYPE_F32 && q_dtype != MOE_DTYPE_BF16)
         return fail(MOE_EINVAL, "paged_attention: q_dtype=%d", q_dtype);
+    if (kv->page_stride > UINT32_MAX)
+        return fail(MOE_EUNSUPPORTED, "paged_attention: page_stride %zu (need below 2^32)", kv->page_stride);
     if ((int64_t)B * Hq > INT32_MAX)
         return fail(MOE_EUNSUPPORTED, "paged_attention: B=%d Hq=%d (need fewer than 2^31 rows)", B, Hq);
     if (!(scale > 0.0f) || !(scale < INFINITY))
@@ -70,7 +72,7 @@ extern "C" int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_d
     AttendParams p{};
     p.k = static_cast<const uint8_t *>(kv->k);
     p.v = static_cast<const uint8_t *>(kv->v);
-    p.page_stride = kv->page_stride;
+    p.page_stride = (uint32_t)kv->page_stride;
     p.k_scale = kv->k_scale;
     p.v_scale = kv->v_scale;
     p.n_pages = kv->n_pages;

@@ -62,7 +62,7 @@ constexpr int kMaxLength = INT32_MAX - 65535;         // places past the last ti
 
 struct AttendParams {
     const uint8_t *k, *v;
-    size_t page_stride;
+    uint32_t page_stride;            // bytes
     const float *k_scale, *v_scale;
     int n_pages, Hkv, D, B;
     FastDiv page;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
 
         // ---- the warp's tiles
         const int row_b = p.D * S::ELT;                            // bytes of a stored row
-        const size_t head_b = (size_t)h * p.page.d * row_b;
+        const uint8_t *k_h = p.k + (size_t)h * p.page.d * row_b, *v_h = p.v + (size_t)h * p.page.d * row_b;
         const int32_t *tab = p.table + (size_t)b * p.max_blocks;
         int ids = 0, ids8 = 0;          // ALIGNED: the pages of 32 tiles; else of rows lane / 4 and 8 more of the next tile
         bool bad = false;
@@ -366,18 +366,21 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                 ids8 = page_of(tok + 8);
             }
         };
+        uint32_t fill = ring_a, read = ring_a;                     // the stages to write and to read next
+        auto next = [&](uint32_t &at) { at = at == ring_a + (NS - 1) * S::STAGE ? ring_a : at + S::STAGE; };
         auto issue = [&](int i) {
             if (i < mine) {
                 const int tok0 = tile0 + (warp + NW * i) * kAttTile;
-                const uint32_t dst = ring_a + (i % NS) * S::STAGE;
+                const uint32_t dst = fill;
+                next(fill);
                 if (ALIGNED) {          // one page: whole rows, row after row
                     const int id = __shfl_sync(0xffffffffu, ids, i & 31);
                     const bool ok0 = (unsigned)id < (unsigned)p.n_pages;
                     const int in = tok0 - p.page.div(tok0) * p.page.d;
                     bad |= !ok0;
                     fetch_ids(i + 1);
-                    const size_t at0 = (ok0 ? (size_t)id : 0) * p.page_stride + head_b + (size_t)in * row_b;
-                    const uint8_t *k0 = p.k + at0, *v0 = p.v + at0;
+                    const uint64_t at0 = (uint64_t)(uint32_t)(ok0 ? id : 0) * p.page_stride + (uint32_t)(in * row_b);
+                    const uint8_t *k0 = k_h + at0, *v0 = v_h + at0;
                     if (ok0 && tok0 >= lo && tok0 + kAttTile <= stop && row_b == CH * 16) {
 #pragma unroll
                         for (int n = 0; n < CH * kAttTile / 32; n++) {
@@ -403,14 +406,15 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                         const bool ok0 = in_page && seen;
                         bad |= seen && !in_page;
                         const int in = tok - p.page.div(tok) * p.page.d;
-                        const size_t at0 = ok0 ? (size_t)id * p.page_stride + head_b + (size_t)in * row_b : 0;
+                        const uint64_t at0 = (uint64_t)(uint32_t)(ok0 ? id : 0) * p.page_stride + (uint32_t)(in * row_b);
+                        const uint8_t *k0 = k_h + at0, *v0 = v_h + at0;
 #pragma unroll
                         for (int n = 0; n < CH / 4; n++) {
                             const int ch = 4 * n + t;
                             const bool ok = ok0 && ch * 16 < row_b;
-                            const size_t at = ok ? at0 + ch * 16 : 0;
-                            copy16(dst + key_at<CH>(r, ch), p.k + at, ok);
-                            copy16(dst + S::TILE_B + value_at<CH>(r, ch), p.v + at, ok);
+                            const int at = ch * 16 < row_b ? ch * 16 : 0;
+                            copy16(dst + key_at<CH>(r, ch), k0 + at, ok);
+                            copy16(dst + S::TILE_B + value_at<CH>(r, ch), v0 + at, ok);
                         }
                     }
                     fetch_ids(i + 1);
@@ -477,7 +481,8 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             issue(i + NS - 1);
             copy_wait<NS - 1>();
             __syncwarp();
-            const uint32_t ks = ring_a + (i % NS) * S::STAGE, vs = ks + S::TILE_B;
+            const uint32_t ks = read, vs = ks + S::TILE_B;
+            next(read);
             const int tok0 = tile0 + (warp + NW * i) * kAttTile;
 
             float sp[2][2][4] = {};                 // two chains of products for each 8 tokens
