@@ -43,7 +43,7 @@
 // What is not exact is split into 16-bit parts that are summed in the fp32
 // accumulator: an fp32 q into three bf16 (24 bits) or two fp16 (22 bits, after
 // a power of two per row); the weights P into three bf16 or two fp16 with an
-// fp32 result, two bf16 (16 bits) or one fp16 (11 bits, 2^14 times the weight
+// fp32 result, two bf16 (16 bits) or one fp16 (11 bits, 2^8 times the weight
 // so that small ones keep them) with a bf16 result, whose own rounding is
 // coarser.  With up to 8 heads the second part rides in the tile's
 // otherwise empty rows 8-15 and costs nothing.
@@ -170,6 +170,10 @@ struct AttendShape {
     static constexpr int NA = FULL ? NQ : (NQ + 1) / 2;       // operand tiles of q
     static constexpr int NB = FULL ? NP : (NP + 1) / 2;       // of the weights
     static constexpr int STEPS = DP / 16;
+    // The weights are 2^LIFT at the reference and pass it by 2^(SLACK - LIFT)
+    // at most before it follows: within fp16's 2^16 for an e4m3 cache (2^-22
+    // of the reference keeps 11 bits), anywhere in bf16.
+    static constexpr float LIFT = F8 ? 8.0f : 0.0f, SLACK = F8 ? 15.0f : 16.0f;
     static constexpr int TILE_B = kAttTile * DP * ELT;        // bytes of a tile's keys
     static constexpr int STAGE = TILE_B + (CH == 12 ? kAttTile * 13 * 16 : TILE_B);
     static constexpr bool HALF_UNIT = DP % 64 != 0;           // the last 32 dimensions are half a unit of values
@@ -545,30 +549,27 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                     }
                 }
             }
-            float f[R];
-            bool moved = false;
+            // The reference need not be the maximum: it follows only when a
+            // score passes it by 2^SLACK, so most tiles take no maximum over
+            // the row's lanes and scale nothing.
+            bool over = false;
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[r], top * c[r] - (F8 ? 14.0f : 0.0f));
-                f[r] = 1.0f;
-                if (mn > m[r]) {
-                    f[r] = exp2_f(m[r] - mn);
-                    m[r] = mn;
-                    moved = true;
-                }
-                const float ref = mn == -INFINITY ? 0.0f : mn;
-                float add = 0.0f;
-#pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    x[r][n] = exp2_f(fmaf(x[r][n], c[r], -ref));
-                    add += x[r][n];
-                }
-                l[r] = fmaf(l[r], f[r], add);
+                const float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                over |= fmaf(top, c[r], -m[r]) > S::SLACK;         // (the first tile: m is -inf)
             }
-            if (__any_sync(0xffffffffu, moved)) {
+            if (__any_sync(0xffffffffu, over)) {
+                float f[R];
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float mn = fmaxf(m[r], top * c[r] - S::LIFT);
+                    f[r] = mn > m[r] ? exp2_f(m[r] - mn) : 1.0f;
+                    m[r] = mn;
+                    l[r] *= f[r];
+                }
 #pragma unroll
                 for (int i2 = 0; i2 < DP / 8; i2++) {
                     o[i2][0] *= f[0];
@@ -576,6 +577,13 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                     o[i2][2] *= f[R - 1];
                     o[i2][3] *= f[R - 1];
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float ref = m[r] == -INFINITY ? 0.0f : m[r];
+#pragma unroll
+                for (int n = 0; n < 4; n++) x[r][n] = exp2_f(fmaf(x[r][n], c[r], -ref));
+                l[r] += (x[r][0] + x[r][1]) + (x[r][2] + x[r][3]);
             }
             // the weights as operand tiles
             uint32_t a[S::NB][4];
