@@ -218,6 +218,14 @@ __device__ __forceinline__ int units_of(int len, int window, int room) {
     return (len - lo + UNIT - 1) / UNIT;
 }
 
+// A row's weight in the even runs: its units, and what it costs to begin one
+// (q, the first table entries and keys, the join of the warps: about as much
+// as two units).  The first kBegin places of a row are no units.  Without
+// them a CTA could be given a dozen rows of one token: 29 windows of 1000
+// took 34 us instead of 25 for one request of length 1 among them.
+constexpr int kBegin = 2;
+__device__ __forceinline__ int weight_of(int units) { return units > 0 ? units + kBegin : 0; }
+
 // Quotient of a 64-bit number that nearly always fits 32 bits.
 __device__ __forceinline__ int quotient(int64_t a, int b) {
     return a >> 31 ? (int)(a / b) : (int)a / b;
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     int64_t sum = 0;
-    for (int b = b0; b < b1; b++) sum += units_of<UNIT>(p.seq[b], p.window, room);
+    for (int b = b0; b < b1; b++) sum += weight_of(units_of<UNIT>(p.seq[b], p.window, room));
     int64_t before = sum;
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, before, o);
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             int64_t at = before;
             int b = b0;
             for (;; b++) {
-                const int n = units_of<UNIT>(p.seq[b], p.window, room);
+                const int n = weight_of(units_of<UNIT>(p.seq[b], p.window, room));
                 if (u < (at + n) * HT) break;
                 at += n;
             }
@@ -311,18 +319,24 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     for (int64_t u = u0; u < u1;) {
         const int full_len = p.seq[b];
         const int nb = units_of<UNIT>(full_len, p.window, room);
-        if (off >= (int64_t)nb * HT) {
+        const int nw = weight_of(nb);
+        if (off >= (int64_t)nw * HT) {
             off = 0;
             b++;
             continue;
         }
-        const int ht = quotient(off, nb), blk = (int)(off - (int64_t)ht * nb);
-        if (p.whole && blk > 0) {              // the row belongs to the CTA that its first unit fell to
-            off += nb - blk;
-            u += nb - blk;
+        const int ht = quotient(off, nw), from = (int)(off - (int64_t)ht * nw);
+        if (p.whole && from > 0) {             // the row belongs to the CTA that its first place fell to
+            off += nw - from;
+            u += nw - from;
             continue;
         }
-        const int n_unit = p.whole ? nb : (int)min((int64_t)(nb - blk), u1 - u);
+        const int n_place = p.whole ? nw : (int)min((int64_t)(nw - from), u1 - u);
+        const int blk = max(0, from - kBegin), n_unit = max(0, from + n_place - kBegin) - blk;
+        const int64_t row_u = u - from;        // the row's first place
+        u += n_place;
+        off += n_place;
+        if (n_unit == 0) continue;             // the row's units are the next CTA's
         const int h = ht / p.tiles, head0 = h * p.G + (ht - h * p.tiles) * ROWS;
         const int n_rows = min(ROWS, (h + 1) * p.G - head0);
         const int len = min(full_len, room);
@@ -703,8 +717,6 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                 if (t == 0 && p.lse) p.lse[(size_t)b * p.Hq + head0 + row] = 0.69314718055994531f * (m[r] + log2f(l[r]));
             }
             __syncwarp();
-            u += n_unit;
-            off += n_unit;
             continue;
         }
         // ---- the warps' parts of the row
@@ -779,7 +791,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             }
         }
         if (tid == 0 && blk == 0 && n_unit < nb) {
-            const int64_t last = u + nb - 1;                       // the row's last unit, and its CTA
+            const int64_t last = row_u + nw - 1;                   // the row's last unit, and its CTA
             const int c1 = (int)(((last + 1) * n_cta - 1) / W);
             p.meta[p.by_row ? b * HT + ht : cta] = make_int4(c1 - cta + 1, b * HT + ht, cta, slot);
         } else if (tid == 0 && blk == 0 && p.by_row && !p.whole) {
@@ -787,8 +799,6 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         }
         __syncthreads();
         first_seg = false;
-        u += n_unit;
-        off += n_unit;
     }
 
     // rows with nothing to see
