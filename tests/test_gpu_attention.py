@@ -225,6 +225,38 @@ def test_append_stores_rounded_rows_and_nothing_else(m, x, cache, N, H, page, D)
     assert torch.equal(got[~at], ref[~at])
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.3, 0.0107421875, 3.0, 1e-30, 2.0 ** -127, 1e38, 3e38, 0.0])
+def test_append_e4m3_rounds_the_exact_quotient(m, scale):
+    """Quotients at and beside every midpoint of two e4m3 numbers, around its
+    smallest and largest ones, and with scales whose reciprocal is no normal
+    number: the bits of the quotient rounded to fp32 and then to e4m3."""
+    H, D, page = 2, 64, 16
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    codes = codes[~codes.isnan()].unique()
+    mid = torch.cat([(codes[1:] + codes[:-1]) / 2, codes, torch.tensor([448.0, 464.0, 480.0, 1e4, 2.0 ** -11, 2.0 ** -40], dtype=torch.float64)])
+    x = (mid * scale).float()
+    near = [x]
+    for toward in (float("inf"), -float("inf")):
+        y = x
+        for _ in range(4):
+            y = torch.nextafter(y, torch.tensor(toward))
+            near.append(y)
+    x = torch.cat(near)
+    x = torch.cat([x, -x, torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan")])])
+    N = -(-x.numel() // (H * D))
+    x = torch.nn.functional.pad(x, (0, N * H * D - x.numel())).view(N, H * D).cuda()
+    P = -(-N // page)
+    kv = torch.zeros((P, 2, H, page, D), dtype=torch.uint8, device="cuda")
+    sc = torch.full((H,), scale, device="cuda")
+    m.moe_kv_append(_desc(m, kv, (sc, sc)), x, x, torch.arange(N, dtype=torch.int32, device="cuda"), N)
+    want = (x / sc[0]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(N, H, D)
+    for part in range(2):
+        got = torch.stack([kv[n // page, part, :, n % page] for n in range(N)])
+        nan = want.float().isnan()
+        assert torch.equal(got.view(torch.float8_e4m3fn).float().isnan(), nan)
+        assert torch.equal(got[~nan], want.view(torch.uint8)[~nan])
+
+
 # ------------------------------------------------------------ attention
 def _attend_case(m, lens, Hq, H, D, page, q_type, cache, window=0, seed=0, split=False, pad=0, P=None, spread=1.0, table_pad=2):
     """Runs one call on a cache whose every number behind the lengths is NaN,
