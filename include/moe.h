@@ -43,6 +43,12 @@
  * route's experts from a host-memory pool into HBM slots, for an expert tier
  * outside HBM), packing, sizes and test hooks.
  *
+ * The rest of a decoder layer at decode time: moe_kv_plan (block tables,
+ * slots and free pages of a scheduler step), moe_kv_append (keys and values
+ * into a paged cache), moe_paged_attention (one new token of each request
+ * over the cache) and moe_scored_route (routing by softmax or sigmoid scores
+ * with a balance bias and groups).
+ *
  * Conventions shared by every call
  *  - Memory: every pointer argument is a DEVICE pointer unless stated
  *    otherwise; the caller owns all memory.  The library never allocates,

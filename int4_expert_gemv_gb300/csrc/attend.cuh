@@ -935,7 +935,7 @@ int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     // its own: a row costs about as much as four tiles of it before its first
     // product, which is then paid for four rows at once.
     const int64_t room = (int64_t)p.max_blocks * p.page.d;
-    const int64_t longest = p.window > 0 && p.window + kAttTile < room ? p.window + kAttTile : room;
+    const int64_t seen = (int64_t)p.window + kAttTile, longest = p.window > 0 && seen < room ? seen : room;
     p.whole = longest <= 4 * S::UNIT;
     if (p.whole) {
         const int64_t tile = (longest + kAttTile - 1) / kAttTile;

@@ -19,7 +19,10 @@
 // Measured 34.8 us with bias and 4 of 8 groups, K = 8: instruction issue
 // bounds it (68 % of the issue slots); a round costs 1.5 us, the groups 4.5,
 // the bias 2, and the rest 17.6.  A warp per token with a warp-wide integer
-// maximum per round took 68 us.
+// maximum per round took 68 us; two or four lanes a token 41 (shared memory
+// then halves the warps of an SM); a block's second choice kept in a register
+// 36, and 64 instead of 50 with K = 16 (some token of the four always has to
+// look for a third).
 #include <cfloat>
 #include <type_traits>
 
