@@ -62,6 +62,7 @@
 
 #include <cuda_fp16.h>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 
 namespace moe {

@@ -16,11 +16,14 @@
 
 #include <cuda_fp8.h>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 
 namespace moe {
 
 namespace {
+
+constexpr int kMaxPlanRequests = 16384;     // their three sums fit shared memory
 
 struct PlanParams {
     const int32_t *seq, *add;

@@ -26,6 +26,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 
 namespace moe {
