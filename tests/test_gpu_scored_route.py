@@ -28,7 +28,8 @@ def _route(m, z, K, score="softmax", n_group=1, keep=1, best=1, renorm=True, fac
 
 def _rule(z, K, score, n_group, keep, best, renorm, factor, bias):
     """(idx, w, margin) of one token in 64 bits; margin: the smallest
-    difference between unequal neighbours of an order that was decided."""
+    difference between a choice that was made and the next unequal one (equal
+    ones go by their index)."""
     E = len(z)
     on = np.isfinite(z) | (z == np.inf)
     s = np.zeros(E)
@@ -46,9 +47,10 @@ def _rule(z, K, score, n_group, keep, best, renorm, factor, bias):
     def order(v, n):
         nonlocal margin
         o = np.argsort(-v, kind="stable")
-        for a, b in zip(o[:n], o[1:n + 1]):
-            if v[a] != v[b] and np.isfinite(v[b]):
-                margin = min(margin, v[a] - v[b])
+        for i in range(n):
+            below = v[o[i:]][v[o[i:]] < v[o[i]]]
+            if len(below) and np.isfinite(below[0]):
+                margin = min(margin, v[o[i]] - below[0])
         return o[:n]
 
     allowed = np.ones(E, bool)
