@@ -239,8 +239,8 @@ constexpr int kBegin = 2;
 __device__ __forceinline__ int weight_of(int units) { return units > 0 ? units + kBegin : 0; }
 
 // Quotient of a 64-bit number that nearly always fits 32 bits.
-__device__ __forceinline__ int quotient(int64_t a, int b) {
-    return a >> 31 ? (int)(a / b) : (int)a / b;
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return a >> 31 ? a / b : (int64_t)((int)a / b);
 }
 
 template <bool QF32>
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     for (int k = 0; k < TEAMS; k++) {          // a thread in whose requests a team's run begins says so
         const int c = blockIdx.x * TEAMS + k;
         if (c >= n_cta) continue;
-        const int64_t u = c * W / n_cta;
+        const int64_t u = quotient(c * W, n_cta);
         if (u >= before * HT && u < (before + sum) * HT) {
             int64_t at = before;
             int b = b0;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     __syncthreads();
 
     const bool busy = cta < n_cta;
-    const int64_t u0 = busy ? cta * W / n_cta : 0, u1 = busy ? (cta + 1) * W / n_cta : 0;
+    const int64_t u0 = busy ? quotient(cta * W, n_cta) : 0, u1 = busy ? quotient((cta + 1) * W, n_cta) : 0;
     int b = busy ? sm_b[team] : 0;
     int64_t off = busy ? sm_off[team] : 0;
     bool first_seg = true;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             b++;
             continue;
         }
-        const int ht = quotient(off, nw), from = (int)(off - (int64_t)ht * nw);
+        const int ht = (int)quotient(off, nw), from = (int)(off - (int64_t)ht * nw);
         if (p.whole && from > 0) {             // the row belongs to the CTA that its first place fell to
             off += nw - from;
             u += nw - from;
@@ -930,17 +930,19 @@ int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     p.ctas = num_sms() * S::CTAS;
     const int64_t rows = (int64_t)p.B * p.Hkv * p.tiles;
     p.by_row = rows <= p.ctas;
-    // Rows of at most four units (by the table's width and the window) are
-    // not cut: a CTA takes those that begin in its run, which costs less than
-    // the join and its launch.  Where there are many, each warp takes rows of
-    // its own: a row costs about as much as four tiles of it before its first
+    // Rows that are short by the table's width and the window are not cut: a
+    // CTA takes those that begin in its run.  That saves the join and its
+    // launch (about four units' time), and costs what the run is uneven by: up
+    // to four units always, and more where the CTAs have rows enough.  Where
+    // there are many rows, each warp takes rows of its own: a row costs about as much as four tiles of it before its first
     // product, which is then paid for four rows at once.
     const int64_t room = (int64_t)p.max_blocks * p.page.d;
     const int64_t seen = (int64_t)p.window + kAttTile, longest = p.window > 0 && seen < room ? seen : room;
-    p.whole = longest <= 4 * S::UNIT;
+    const int64_t units = (longest + S::UNIT - 1) / S::UNIT, rounds = (rows + p.ctas - 1) / p.ctas;
+    p.whole = units <= 4 || (units <= 64 && rounds * (units + kBegin) <= rows * (units + kBegin) / p.ctas + 5);
     if (p.whole) {
         const int64_t tile = (longest + kAttTile - 1) / kAttTile;
-        const int64_t shared = (rows + p.ctas - 1) / p.ctas * (4 + (tile + 3) / 4);
+        const int64_t shared = rounds * (4 + units);
         const int64_t solo = (rows + 4 * p.ctas - 1) / (4 * p.ctas) * (4 + tile);
         return solo < shared ? launch_attend_rows<DP, F8, QF32, FULL, ALIGNED, true>(p, st)
                              : launch_attend_rows<DP, F8, QF32, FULL, ALIGNED, false>(p, st);
