@@ -7,22 +7,23 @@
 // one lane reads 32 or 16 bytes of a row, its neighbours the next ones.  A
 // lane keeps each of its blocks' largest choice in a register and all
 // choices in shared memory.  A round of the top-K is then a maximum over a
-// lane's blocks and over LT lanes; only the lane that had it looks into
-// that one block again.  With 8 lanes a warp does so for four tokens at
-// once, which is what the rounds cost most of; with 32 a token has the
-// shorter chain.  Choices are floats: what is off is -FLT_MAX (all other
-// choices are kept at or above it), what is taken or dropped -inf.
+// lane's blocks and over LT lanes, and the chosen block's eight before eight
+// lanes: which one it was, and the largest that is left.  With 8 lanes a warp
+// does so for four tokens at once, which is what the rounds cost most of;
+// with 32 a token has the shorter chain.  Choices are floats: what is off is
+// -FLT_MAX (all other choices are kept at or above it), what is taken or
+// dropped -inf.
 //
 // Bound.  The logits are read once (4 E bytes a token, 10.5 us for 65521
 // tokens of 256 at the copy rate) and each costs an exponential and a
 // reciprocal for its sigmoid: 16 of those a clock and SM make 7 us there.
-// Measured 34.8 us with bias and 4 of 8 groups, K = 8: instruction issue
-// bounds it (68 % of the issue slots); a round costs 1.5 us, the groups 4.5,
-// the bias 2, and the rest 17.6.  A warp per token with a warp-wide integer
-// maximum per round took 68 us; two or four lanes a token 41 (shared memory
-// then halves the warps of an SM); a block's second choice kept in a register
-// 36, and 64 instead of 50 with K = 16 (some token of the four always has to
-// look for a third).
+// Measured 33 us with bias and 4 of 8 groups, K = 8: instruction issue bounds
+// it; a round costs 1.4 us, the groups 3.4, the bias 2, and the rest 18.  A
+// warp per token with a warp-wide integer maximum per round took 68 us; two or
+// four lanes a token 41 (shared memory then halves the warps of an SM); the
+// lane of a block going through its eight alone 35; a block's second choice
+// kept in a register 36, and 64 instead of 46 with K = 16 (some token of the
+// four always has to look for a third).
 #include <cfloat>
 #include <type_traits>
 
@@ -278,19 +279,24 @@ __global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const Route
             before[i] = 0;
         }
         uint32_t kept = 0;
-#pragma unroll
-        for (int i = 0; i < GL; i++) {
-            if (LT * i >= p.n_group) break;
+        if (p.n_group <= LT) {                      // a group a lane
 #pragma unroll
             for (int k = 0; k < LT; k++) {
-                const int other = k + LT * i;
-                const float o = __shfl_sync(0xffffffffu, score[i], (lane & ~(LT - 1)) + k);
-                if (other < p.n_group) {
-#pragma unroll
-                    for (int a = 0; a < GL; a++)
-                        before[a] += o > score[a] || (o == score[a] && other < l + LT * a);
-                }
+                const float o = __shfl_sync(0xffffffffu, score[0], (lane & ~(LT - 1)) + k);
+                if (k < p.n_group) before[0] += o > score[0] || (o == score[0] && k < l);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < GL; i++)
+                for (int k = 0; k < LT; k++) {
+                    const int other = k + LT * i;
+                    const float o = __shfl_sync(0xffffffffu, score[i], (lane & ~(LT - 1)) + k);
+                    if (other < p.n_group) {
+#pragma unroll
+                        for (int a = 0; a < GL; a++)
+                            before[a] += o > score[a] || (o == score[a] && other < l + LT * a);
+                    }
+                }
         }
 #pragma unroll
         for (int a = 0; a < GL; a++)
@@ -304,6 +310,7 @@ __global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const Route
         }
     }
 
+    __syncwarp();                                   // the choices, for all lanes
     const uint32_t seg = LT == 32 ? 0xffffffffu : ((1u << (LT & 31)) - 1u) << (lane & ~(LT - 1));
     for (int k = 0; k < p.K; k++) {
         float v = top[0];                           // this lane's best block, the first of equals
@@ -323,27 +330,26 @@ __global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const Route
             for (int o = LT / 2; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
             who = __ballot_sync(0xffffffffu, v == best && s == low) & seg;
         }
-        if (lane == __ffs(who) - 1) {
-            float f[8], n = 0.0f;
-            get8(s, f);
-            int at = 0;
+        // its eight lie before eight lanes: which one it was, and what is left
+        const int src = __ffs(who) - 1, block = __shfl_sync(0xffffffffu, s, src), i = l & 7;
+        float *mine_c = c_s + (i >> 2) * NB * 4 + block * 4 + (i & 3);
+        const float c = *mine_c;
+        const uint32_t eq = __ballot_sync(0xffffffffu, c == best) >> (lane & ~(LT - 1)) & 0xffu;
+        const int at = __ffs(eq) - 1;
+        float next = i == at ? -INFINITY : c;
 #pragma unroll
-            for (int i = 7; i >= 0; i--)
-                if (f[i] == best) {
-                    at = i;
-                    f[i] = -INFINITY;
-                    n += 1.0f;
-                }
-            float next = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
-            if (n > 1.0f) next = best;              // its equals are left
-            c_s[(at >> 2) * NB * 4 + s * 4 + (at & 3)] = -INFINITY;
-            pick_s[k] = s * 8 + at;
+        for (int o = 4; o > 0; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, o));
+        if (l == at) {
+            *mine_c = -INFINITY;
+            pick_s[k] = block * 8 + at;
+        }
+        if (lane == src) {
 #pragma unroll
             for (int j = 0; j < SUB; j++)
                 if (j == mine) top[j] = next;
         }
+        __syncwarp();
     }
-    __syncwarp();
 
     constexpr int KL = (16 + LT - 1) / LT;
     float w[KL], sum = 0.0f;
