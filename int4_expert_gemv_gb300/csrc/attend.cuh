@@ -20,10 +20,10 @@
 // key or value number is used by G heads, 2 G flops for 2 bytes (bf16): far
 // below the machine's balance, so the design aims at bytes in flight and few
 // instructions per byte, and the products go to the tensor cores only to stay
-// out of the way.  mma.sync with
-// its 16-row tile and register operands fits that: a tcgen05 tile has 64
-// rows or more of which G would be used, and its accumulator would have to
-// come out of tensor memory for every 64 tokens' softmax.
+// out of the way.  mma.sync with its 16-row tile and register operands fits
+// that: a tcgen05 tile has 64 rows or more of which G would be used, and its
+// accumulator would have to come out of tensor memory for every 64 tokens'
+// softmax.
 //
 // Work split.  The unit is 64 tokens (16 for each of four warps) of one
 // (request, key head): a row.  All units, in order of requests, heads and
@@ -59,6 +59,8 @@
 // coarser.  With up to 8 heads the second part rides in the tile's
 // otherwise empty rows 8-15 and costs nothing.
 #pragma once
+
+#include <cfloat>
 
 #include <cuda_fp16.h>
 
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
                     c *= __uint_as_float((uint32_t)max(1, e - 13) << 23);
                 }
             }
+            if (c < FLT_MIN) c = FLT_MIN;     // a scale of 0: alike weights, and no 0 times a masked -inf
             if (lane == 0) sm_c[team][r] = c;
 #pragma unroll
             for (int i = 0; i < IT; i++) {
@@ -932,14 +935,17 @@ int launch_attend_kernel(AttendParams p, cudaStream_t st) {
     p.by_row = rows <= p.ctas;
     // Rows that are short by the table's width and the window are not cut: a
     // CTA takes those that begin in its run.  That saves the join and its
-    // launch (about four units' time), and costs what the run is uneven by: up
-    // to four units always, and more where the CTAs have rows enough.  Where
-    // there are many rows, each warp takes rows of its own: a row costs about as much as four tiles of it before its first
-    // product, which is then paid for four rows at once.
+    // launch (about five units' time), and costs what the run is uneven by: up
+    // to four units always, up to eight where the CTAs have rows enough (32
+    // requests of up to 500 tokens, 8 key heads: 10.5 us against 12.5).  Where
+    // there are many rows, each warp takes rows of its own: a row costs about
+    // as much as four tiles of it before its first product, which is then paid
+    // for four rows at once (199 requests of up to 3 tokens, heads of 192: 14
+    // us against 27).
     const int64_t room = (int64_t)p.max_blocks * p.page.d;
     const int64_t seen = (int64_t)p.window + kAttTile, longest = p.window > 0 && seen < room ? seen : room;
     const int64_t units = (longest + S::UNIT - 1) / S::UNIT, rounds = (rows + p.ctas - 1) / p.ctas;
-    p.whole = units <= 4 || (units <= 64 && rounds * (units + kBegin) <= rows * (units + kBegin) / p.ctas + 5);
+    p.whole = units <= 4 || (units <= 8 && rounds * (units + kBegin) <= rows * (units + kBegin) / p.ctas + 5);
     if (p.whole) {
         const int64_t tile = (longest + kAttTile - 1) / kAttTile;
         const int64_t shared = rounds * (4 + units);

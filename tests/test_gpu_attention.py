@@ -408,6 +408,16 @@ def test_attention_never_reads_through_a_bad_page_or_past_the_table(m):
         _check(c, skip=(3,))
 
 
+@pytest.mark.parametrize("q", [torch.bfloat16, torch.float32])
+def test_attention_of_scales_of_zero_and_below(m, q):
+    """Key scales of 0 (every weight alike) and below 0, and a value scale of
+    0, with tiles that are partly masked."""
+    c = _attend_case(m, [1, 5, 100, 333], 8, 4, 64, 16, q, torch.float8_e4m3fn, window=77, seed=3)
+    c["sc"][0][0], c["sc"][0][1], c["sc"][1][2] = 0.0, -0.02, 0.0
+    _call(m, c)
+    _check(c)
+
+
 def test_attention_without_lse_and_of_no_rows(m):
     c = _attend_case(m, [70, 3], 4, 2, 64, 16, torch.bfloat16, torch.bfloat16)
     _call(m, c)
