@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     constexpr int THREADS = 32 * kAttWarps, TEAMS = kAttWarps / NW;       // a team: the warps of a row
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sm_sum[kAttWarps];
+    __shared__ int sm_top[kAttWarps];
     __shared__ int64_t sm_off[TEAMS];
     __shared__ int sm_b[TEAMS], sm_bad;
     __shared__ float sm_c[TEAMS][16];
@@ -285,13 +286,22 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     int64_t sum = 0;
-    for (int b = b0; b < b1; b++) sum += weight_of(units_of<UNIT>(p.seq[b], p.window, room));
+    int top_w = 0;
+    for (int b = b0; b < b1; b++) {
+        const int w = weight_of(units_of<UNIT>(p.seq[b], p.window, room));
+        sum += w;
+        top_w = max(top_w, w);
+    }
+    top_w = __reduce_max_sync(0xffffffffu, top_w);
     int64_t before = sum;
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += u;
     }
-    if (lane == 31) sm_sum[wrp] = before;
+    if (lane == 31) {
+        sm_sum[wrp] = before;
+        sm_top[wrp] = top_w;
+    }
     before -= sum;
     for (int i = tid; i < TEAMS * S::Q_B / 16; i += THREADS)
         reinterpret_cast<uint4 *>(smem + kAttWarps * S::RING)[i] = make_uint4(0, 0, 0, 0);
@@ -301,11 +311,21 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     for (int w = 0; w < kAttWarps; w++) {
         if (w == wrp) before += W;
         W += sm_sum[w];
+        top_w = max(top_w, sm_top[w]);
     }
     W *= HT;
     // a unit for each team while that makes at most 64 parts of a row, then four
     const int n_cta = (int)min((int64_t)p.ctas * TEAMS, max(W / 4, min(W, (int64_t)p.B * HT * 64)));
     if (tid == 0 && !p.by_row && !p.whole) p.meta[cta] = make_int4(0, 0, 0, 0);
+    // Rows are not cut either where the lengths turn out to give each CTA one
+    // row or less and the longest is little more than an even run: a CTA's two
+    // parts and the join cost six units' time (32 requests of 1000 tokens, 8
+    // key heads: 29 us cut).
+    bool whole_rows = p.whole;
+    if (!SOLO && !p.whole && n_cta > 0) {
+        const int64_t each = quotient(W, n_cta);
+        whole_rows = each <= top_w && top_w <= each + 6;
+    }
 #pragma unroll
     for (int k = 0; k < TEAMS; k++) {          // a thread in whose requests a team's run begins says so
         const int c = blockIdx.x * TEAMS + k;
@@ -340,12 +360,12 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             continue;
         }
         const int ht = (int)quotient(off, nw), from = (int)(off - (int64_t)ht * nw);
-        if (p.whole && from > 0) {             // the row belongs to the CTA that its first place fell to
+        if (whole_rows && from > 0) {             // the row belongs to the CTA that its first place fell to
             off += nw - from;
             u += nw - from;
             continue;
         }
-        const int n_place = p.whole ? nw : (int)min((int64_t)(nw - from), u1 - u);
+        const int n_place = whole_rows ? nw : (int)min((int64_t)(nw - from), u1 - u);
         const int blk = max(0, from - kBegin), n_unit = max(0, from + n_place - kBegin) - blk;
         const int64_t row_u = u - from;        // the row's first place
         u += n_place;
