@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sm_sum[kAttWarps];
     __shared__ int sm_top[kAttWarps];
-    __shared__ int64_t sm_off[TEAMS];
+    __shared__ int64_t sm_off[TEAMS], sm_W, sm_end;
     __shared__ int sm_b[TEAMS], sm_bad;
     __shared__ float sm_c[TEAMS][16];
     __shared__ float2 sm_ml[kAttWarps][16];
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             sm_off[k] = u - at * HT;
         }
     }
+    if (tid == 0) sm_W = W;                    // (for a cut row's last CTA; not kept in registers meanwhile)
     __syncthreads();
 
     const bool busy = cta < n_cta;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         }
         const int n_place = whole_rows ? nw : (int)min((int64_t)(nw - from), u1 - u);
         const int blk = max(0, from - kBegin), n_unit = max(0, from + n_place - kBegin) - blk;
-        const int64_t row_u = u - from;        // the row's first place
+        const int64_t row_end = u - from + nw;
         u += n_place;
         off += n_place;
         if (n_unit == 0) continue;             // the row's units are the next CTA's
@@ -379,7 +380,10 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
         const int stop = min(len, tile0 + n_unit * UNIT);
         const int n_tile = (stop - tile0 + kAttTile - 1) / kAttTile;
         const int mine = n_tile > warp ? (n_tile - warp + NW - 1) / NW : 0;
-        if (!SOLO && tid == 0) sm_bad = full_len > room;
+        if (!SOLO && tid == 0) {
+            sm_bad = full_len > room;
+            sm_end = row_end;
+        }
 
         // ---- q: the numbers are loaded before the first tiles are asked for, and split after
         constexpr int QR = ROWS / NW, IT = (DP / 4 + 31) / 32;
@@ -826,8 +830,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, (AttendShape<DP, F8, QF32, FUL
             }
         }
         if (tid == 0 && blk == 0 && n_unit < nb) {
-            const int64_t last = row_u + nw - 1;                   // the row's last unit, and its CTA
-            const int c1 = (int)(((last + 1) * n_cta - 1) / W);
+            const int c1 = (int)((sm_end * n_cta - 1) / sm_W);     // the CTA of the row's last unit
             p.meta[p.by_row ? b * HT + ht : cta] = make_int4(c1 - cta + 1, b * HT + ht, cta, slot);
         } else if (tid == 0 && blk == 0 && p.by_row && !p.whole) {
             p.meta[b * HT + ht] = make_int4(0, 0, 0, 0);
