@@ -17,13 +17,14 @@
 // Bound.  The logits are read once (4 E bytes a token, 10.5 us for 65521
 // tokens of 256 at the copy rate) and each costs an exponential and a
 // reciprocal for its sigmoid: 16 of those a clock and SM make 7 us there.
-// Measured 33 us with bias and 4 of 8 groups, K = 8: instruction issue bounds
-// it; a round costs 1.4 us, the groups 3.4, the bias 2, and the rest 18.  A
-// warp per token with a warp-wide integer maximum per round took 68 us; two or
-// four lanes a token 41 (shared memory then halves the warps of an SM); the
-// lane of a block going through its eight alone 35; a block's second choice
-// kept in a register 36, and 64 instead of 46 with K = 16 (some token of the
-// four always has to look for a third).
+// Measured 32 us with bias and 4 of 8 groups, K = 8: issue slots (64 % taken)
+// and the latencies of shared memory and shuffles share it; a round costs 1.4
+// us, the groups 3.5, the bias 2, and the rest 17.  A warp per token with a
+// warp-wide integer maximum per round took 68 us; two or four lanes a token 41
+// (shared memory then halves the warps of an SM); the lane of a block going
+// through its eight alone 35; a block's second choice kept in a register 36,
+// and 64 instead of 45 with K = 16 (some token of the four always has to look
+// for a third); the row asked for ahead into L2 33.
 #include <cfloat>
 #include <type_traits>
 
@@ -40,6 +41,7 @@ struct RouteParams {
     int T, E, K, n_group, gs, nsub, keep, best, renorm;   // gs: experts of a group, nsub: blocks of a token
     FastDiv spg;                                          // blocks of a group
     int vec;                                              // whole blocks, 16-byte aligned
+    int tok;                                              // floats of a token in shared memory
     float factor;
     const float *bias;
     int32_t *idx;
@@ -108,22 +110,23 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // Shared memory of a token: its choices (the first, then the second float4 of
-// every block, so that neighbouring lanes meet no bank twice), the blocks'
-// best two, the places of the chosen.
-__host__ __device__ constexpr int route_token_floats(int LT, int SUB) { return LT * SUB * 10 + 16; }
+// every block, so that neighbouring lanes meet no bank twice), with groups the
+// blocks' best two, the places of the chosen.
+inline int route_token_floats(int nsub, bool groups) { return nsub * 8 + (groups ? (nsub + 1) / 2 * 4 : 0) + 16; }
 
 template <typename X, int LT, int SUB, bool SIGMOID, bool VEC>
-__global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route_kernel(const RouteParams p) {
     extern __shared__ __align__(16) float smem[];
-    constexpr int TOK = kRouteThreads / LT, NB = LT * SUB;
+    constexpr int TOK = kRouteThreads / LT;
+    const int NB = p.nsub;
     const int lane = threadIdx.x & 31, sub = threadIdx.x / LT, l = threadIdx.x % LT;
     const int tt = blockIdx.x * TOK + sub;
     const bool live = tt < p.T;
     const int t = live ? tt : p.T - 1;             // the last warp's idle lanes repeat a token
-    float *c_s = smem + sub * route_token_floats(LT, SUB);
+    float *c_s = smem + sub * p.tok;
     float4 *c4 = reinterpret_cast<float4 *>(c_s);
     float2 *best_s = reinterpret_cast<float2 *>(c_s + NB * 8);
-    int *pick_s = reinterpret_cast<int *>(c_s + NB * 10);
+    int *pick_s = reinterpret_cast<int *>(c_s + p.tok - 16);
     const X *row = static_cast<const X *>(p.z) + (size_t)t * p.stride;
     const bool groups = p.keep < p.n_group;
 
@@ -380,13 +383,12 @@ __global__ void __launch_bounds__(kRouteThreads) scored_route_kernel(const Route
 template <typename X, bool SIGMOID, int LT, int SUB>
 int launch_sub(const RouteParams &p, cudaStream_t st) {
     constexpr int TOK = kRouteThreads / LT;
-    constexpr size_t smem = (size_t)TOK * route_token_floats(LT, SUB) * sizeof(float);
-    static_assert(smem <= 200 * 1024, "shared memory of a CTA");
+    const size_t smem = (size_t)TOK * p.tok * sizeof(float);        // at most 16 tokens of 155 blocks: 107 KB
     auto kernel = p.vec ? scored_route_kernel<X, LT, SUB, SIGMOID, true> : scored_route_kernel<X, LT, SUB, SIGMOID, false>;
     if (smem > 48 * 1024) {
         static OnDevices ready[2];
         const cudaError_t e = ready[p.vec].once(
-            [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
+            [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024); });
         if (e != cudaSuccess) return fail(MOE_ECUDA, "scored_route_kernel: %s", cudaGetErrorString(e));
     }
     kernel<<<(unsigned)((p.T + TOK - 1) / TOK), kRouteThreads, smem, st>>>(p);
@@ -411,8 +413,9 @@ int launch_lt(const RouteParams &p, cudaStream_t st) {
 template <typename X, bool SIGMOID>
 int launch_route(const RouteParams &p, cudaStream_t st) {
     // 32 lanes a token while that does not fill the SMs.  Measured, 32 against
-    // 8 lanes: 1 x 256 3.7 / 5.7 us, 2525 x 160 5.2 / 5.5, 4096 x 512 5.3 /
-    // 6.5, but 4433 x 60 5.4 / 3.2, 9028 x 64 9.1 / 3.8, 65521 x 256 80 / 35.
+    // 8 lanes (tokens x experts): 1 x 256 3.7 / 5.7 us, 2525 x 160 5.2 / 5.5,
+    // 4096 x 512 5.3 / 6.5, but 4433 x 60 5.4 / 3.2, 9028 x 64 9.1 / 3.8,
+    // 65521 x 256 80 / 35.
     const int most = num_sms() * (p.nsub > 16 ? 32 : 8);
     return p.T <= most ? launch_lt<X, SIGMOID, 32>(p, st) : launch_lt<X, SIGMOID, 8>(p, st);
 }
@@ -464,6 +467,7 @@ extern "C" int moe_scored_route(const moe_route_desc *rd, const void *logits, in
     p.keep = groups ? rd->keep_group : 1;
     p.spg = FastDiv((p.gs + 7) / 8);
     p.nsub = p.n_group * p.spg.d;
+    p.tok = route_token_floats(p.nsub, groups);
     p.best = rd->group_best;
     p.renorm = rd->renorm != 0;
     p.vec = p.gs % 8 == 0 && stride * elt % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
