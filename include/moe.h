@@ -342,8 +342,9 @@ int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const v
  * [0, n_pages), or a length above max_blocks * page (or 2^31 - 2^16), is never
  * read through: that request's out and lse are NaN.
  * Scores, statistics and sums in fp32; products on the tensor cores from
- * numbers split so that an fp32 q and the softmax's weights keep fp32's
- * accuracy (with a BF16 result at least 2^-11 before it is rounded).
+ * numbers split into parts: an fp32 q and the softmax's weights keep 24 bits
+ * (22 over an E4M3 cache); with a BF16 result over a BF16 cache the weights
+ * keep 16.
  * The same inputs give the same bits on the same device.
  * ws: moe_paged_attention_workspace_bytes() bytes, 256-byte aligned, no
  * clearing needed. */

@@ -53,11 +53,13 @@
 // Accuracy.  bf16 and e4m3 keys and values are exact operands (e4m3 as fp16).
 // What is not exact is split into 16-bit parts that are summed in the fp32
 // accumulator: an fp32 q into three bf16 (24 bits) or two fp16 (22 bits, after
-// a power of two per row); the weights P into three bf16 or two fp16 with an
-// fp32 result, two bf16 (16 bits) or one fp16 (11 bits, 2^8 times the weight
-// so that small ones keep them) with a bf16 result, whose own rounding is
-// coarser.  With up to 8 heads the second part rides in the tile's
-// otherwise empty rows 8-15 and costs nothing.
+// a power of two per row); the weights P into three bf16 with an fp32 result
+// over a bf16 cache, two bf16 (16 bits) with a bf16 result, two fp16 (22 bits,
+// of 2^8 times the weight so that small ones keep them) over an e4m3 cache.
+// With up to 8 heads the second part rides in the tile's otherwise empty rows
+// 8-15 and costs nothing; with more it is a tile of its own (64 requests, 12
+// heads of 64 over e4m3: 66.9 us, 60.2 with the first part alone; heads of
+// 128: no difference).
 #pragma once
 
 #include <cfloat>
@@ -179,7 +181,7 @@ struct AttendShape {
     static constexpr int ELT = F8 ? 1 : 2;
     static constexpr int CH = DP * ELT / 16;                  // 16-byte chunks of a row
     static constexpr int NQ = QF32 ? (F8 ? 2 : 3) : 1;        // parts of q
-    static constexpr int NP = QF32 ? (F8 ? 2 : 3) : (F8 ? 1 : 2);   // parts of the weights
+    static constexpr int NP = QF32 && !F8 ? 3 : 2;            // parts of the weights
     static constexpr int ROWS = FULL ? 16 : 8;                // query heads of a tile
     static constexpr int NA = FULL ? NQ : (NQ + 1) / 2;       // operand tiles of q
     static constexpr int NB = FULL ? NP : (NP + 1) / 2;       // of the weights

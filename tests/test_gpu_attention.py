@@ -534,3 +534,36 @@ def test_plan_append_attend_together(m):
             # bf16's half unit, and 2^-12 + 2^-18 of the largest value for the weights and scores
             tol = 2.0 ** -8 * ref.abs() + (2.0 ** -12 + 2.0 ** -18) * vv.abs().amax()
             assert ((out[r].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("Hq", [1, 8, 12, 16, 20])
+def test_attention_weights_keep_sixteen_bits(m, cache, Hq):
+    """Two tokens of nearly one score and of opposite values: the result is
+    small beside the values, so what counts is the weights' rounding and not
+    the result's own.  Bound: as above, with 2^-16 for the weights (2^-17 each
+    where they are rounded to 16 bits, and the sum of them as much)."""
+    c = _attend_case(m, [2, 2, 2], Hq, 1, 64, 16, torch.bfloat16, cache, seed=Hq)
+    c["scale"] = 1.0
+    c["q"].zero_()
+    c["q"][:, :, 0] = (2.0 ** -6 * (1 + torch.arange(3 * Hq, device="cuda") / (2.0 * Hq))).view(3, Hq).bfloat16()
+    one, most = (1.0, 4.0) if cache == torch.bfloat16 else (64.0, 448.0)
+    for b in range(3):
+        page = c["kv"][int(c["table"][b, 0])].view(2, 1, 16, 64)
+        rows = torch.zeros((2, 2, 64), device="cuda")
+        rows[0, 0, 0] = one
+        rows[1, 0], rows[1, 1] = most, -most
+        page.view(torch.uint8)[:, 0, :2] = rows.to(cache).view(torch.uint8)
+    _call(m, c)
+    D, G = 64, Hq
+    for b in range(3):
+        p = int(c["table"][b, 0])
+        k, v = c["kv"][p, 0, 0, :2].double(), c["kv"][p, 1, 0, :2].double()
+        if c["sc"][0] is not None:
+            k, v = k * c["sc"][0].double(), v * c["sc"][1].double()
+        x = c["q"][b].double() @ k.T
+        ref = torch.softmax(x, 1) @ v
+        dx = 2.0 ** -21 * x.abs().amax(1, keepdim=True)
+        tol = (2 * dx + 2.0 ** -20 + 2.0 ** -16) * v.abs().amax() + 2.0 ** -8 * ref.abs()
+        err = (c["o"][b].double() - ref).abs()
+        assert (err <= tol).all(), float((err / tol).max())
