@@ -66,18 +66,30 @@ class PagedCache:
 
     def plan(self, new_len: torch.Tensor, most: int | None = None) -> None:
         """new_len int32 [R] on the device: tokens that each request adds, -1
-        for one that has ended; `most`: of all together (max_new).  self.status
-        tells afterwards whether it fit."""
+        for one that has ended; `most`: of all together, at most max_new (the
+        places there are in `slots` and `places`, all of which the call
+        writes).  self.status tells afterwards whether it fit."""
+        most = self.max_new if most is None else most
+        if not 0 <= most <= self.max_new:
+            raise ValueError(f"at most {most} new tokens in a cache with places for {self.max_new}")
+        if (new_len.dtype != torch.int32 or new_len.numel() < self.R or not new_len.is_contiguous()
+                or new_len.device != self.table.device):
+            raise ValueError(f"new_len: int32 [{self.R}] on {self.table.device} needed, got {new_len.dtype} "
+                             f"{tuple(new_len.shape)} on {new_len.device}")
         a, b = self._now, 1 - self._now
         moe.moe_kv_plan(self.lengths[a], new_len, self.R, self.table, self.max_blocks, self.page,
                         self.ring, self.n_pages, self.pool[a], self.lengths[b], self.first,
-                        self.slots, self.places,
-                        self.max_new if most is None else most, self.pool[b], self.status)
+                        self.slots, self.places, most, self.pool[b], self.status)
         self._now = b
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """k, v [N][Hkv * D] of the plan's new tokens, in order of requests."""
-        moe.moe_kv_append(self.desc, k, v, self.slots, k.shape[0])
+        n, row = k.shape[0], self.desc.Hkv * self.desc.D
+        if n > self.max_new:
+            raise ValueError(f"{n} tokens for {self.max_new} slots")
+        if k.numel() != n * row or v.shape[0] != n or v.numel() != n * row:
+            raise ValueError(f"k and v: [N][{row}] needed, got {tuple(k.shape)} and {tuple(v.shape)}")
+        moe.moe_kv_append(self.desc, k, v, self.slots, n)
 
 
 def rotate(x: torch.Tensor, places: torch.Tensor) -> torch.Tensor:
@@ -121,11 +133,13 @@ class PagedDecoder:
 
     def step(self, x: torch.Tensor, rows: torch.Tensor, new_len: torch.Tensor) -> torch.Tensor:
         """One token for each of the requests in `rows` (int64, ascending; the
-        ones whose new_len is 1).  x fp32 [R][d]: the residual stream; the
+        ones whose new_len is 1; at most the cache's max_new).  x fp32 [R][d]: the residual stream; the
         result is the layer's, valid in those rows.  Nothing here waits for
         the GPU."""
         ca, c, R = self.cache, self.cfg, self.cache.R
-        ca.plan(new_len, R)
+        if rows.numel() > ca.max_new:
+            raise ValueError(f"{rows.numel()} tokens in a step of a cache with places for {ca.max_new}")
+        ca.plan(new_len, min(R, ca.max_new))
         xn = (x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)).bfloat16()
         qkv = xn @ self.w_qkv
         q = qkv[:, : self.Hq * self.D].view(R, self.Hq, self.D)
