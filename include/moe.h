@@ -301,18 +301,19 @@ typedef struct {
  * appended to the rows of block_table; returned pages go behind its end (they
  * are free from the next call on).  The call writes
  *   block_table, ring  only their new entries;
- *   seq_out [R]        seq_len + new_len, 0 for an ended request (not
- *                      seq_len itself);
+ *   seq_out [R]        seq_len + new_len, 0 for an ended request;
  *   first [R + 1]      the first new token of each request, then their count;
  *   slots [cap]        the new tokens' slots in order of requests, then -1;
  *   places [cap]       their places in their requests, then 0;
- *   pool_out [2]       the ring's state after the step (not pool);
+ *   pool_out [2]       the ring's state after the step;
  *   status [1]         MOE_OK; MOE_ENOSPACE when the free pages, a row of
  *                      max_blocks entries or cap do not suffice; MOE_EINVAL
  *                      for a negative length, a new_len below -1, or a pool or
  *                      length outside its range.  Then nothing is taken:
  *                      seq_out = seq_len, first and places 0, slots -1,
  *                      pool_out = pool.
+ * Outputs stand apart from what is read (seq_len, new_len, pool, block_table,
+ * ring; these two from the other inputs as well): an overlap is refused.
  * A page id outside [0, n_pages) gives slots of -1.  page as in moe_kv_desc;
  * n_pages * page < 2^31; all arrays int32 on the device. */
 int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R, int32_t *block_table,

@@ -416,6 +416,18 @@ using namespace moe;
 
 static bool off4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
 
+namespace {
+struct Ints {                        // an array of the plan's
+    const char *name;
+    const int32_t *at;
+    size_t n;
+    bool overlaps(const Ints &o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+        return n > 0 && o.n > 0 && a < b + 4 * o.n && b < a + 4 * n;
+    }
+};
+}  // namespace
+
 extern "C" int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R,
                            int32_t *block_table, int max_blocks, int page, int32_t *ring,
                            int n_pages, const int32_t *pool, int32_t *seq_out, int32_t *first,
@@ -433,8 +445,18 @@ extern "C" int moe_kv_plan(const int32_t *seq_len, const int32_t *new_len, int R
     if (off4(seq_len) || off4(new_len) || off4(block_table) || off4(ring) || off4(pool) ||
         off4(seq_out) || off4(first) || off4(slots) || off4(places) || off4(pool_out) || off4(status))
         return fail(MOE_EINVAL, "kv_plan: misaligned pointer");
-    if ((R > 0 && (seq_out == seq_len || first == seq_len || first == new_len)) || pool_out == pool)
-        return fail(MOE_EINVAL, "kv_plan: an output is an input");
+    // Every CTA reads the lengths, the pool's state, the table and the ring
+    // while others write the outputs.
+    const Ints in[] = {{"seq_len", seq_len, (size_t)R}, {"new_len", new_len, (size_t)R}, {"pool", pool, 2},
+                       {"block_table", block_table, (size_t)R * max_blocks}, {"ring", ring, (size_t)n_pages}};
+    const Ints out[] = {{"seq_out", seq_out, (size_t)R}, {"first", first, (size_t)R + 1}, {"slots", slots, (size_t)cap},
+                        {"places", places, (size_t)cap}, {"pool_out", pool_out, 2}, {"status", status, 1}};
+    for (const Ints &o : out)
+        for (const Ints &i : in)
+            if (o.overlaps(i)) return fail(MOE_EINVAL, "kv_plan: %s overlaps %s", o.name, i.name);
+    for (int j = 3; j < 5; j++)
+        for (int i = 0; i < j; i++)
+            if (in[j].overlaps(in[i])) return fail(MOE_EINVAL, "kv_plan: %s overlaps %s", in[j].name, in[i].name);
     const PlanParams p{seq_len, new_len, R, block_table, max_blocks, FastDiv(page), ring, n_pages,
                        pool, seq_out, first, slots, places, cap, pool_out, status};
     return R > 1024 ? launch_plan<1024>(p, stream) : launch_plan<512>(p, stream);

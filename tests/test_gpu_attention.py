@@ -567,3 +567,25 @@ def test_attention_weights_keep_sixteen_bits(m, cache, Hq):
         tol = (2 * dx + 2.0 ** -20 + 2.0 ** -16) * v.abs().amax() + 2.0 ** -8 * ref.abs()
         err = (c["o"][b].double() - ref).abs()
         assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_plan_of_arrays_that_stand_side_by_side(m):
+    """All eleven in one allocation, none overlapping: nothing is refused."""
+    R, mb, page, P, cap = 5, 4, 8, 30, 40
+    sizes = dict(seq=R, new=R, table=R * mb, ring=P, pool=2, so=R, fi=R + 1, sl=cap, pl=cap, po=2, st=1)
+    slab, at = torch.full((sum(sizes.values()),), 9, dtype=torch.int32, device="cuda"), 0
+    a = {}
+    for k, n in sizes.items():
+        a[k], at = slab[at: at + n], at + n
+    a["seq"].copy_(_ints([0, 8, 3, 0, 31]))
+    a["new"].copy_(_ints([9, 1, 0, 4, 1]))
+    a["table"].copy_(_ints([-1] * 4 + [7, -1, -1, -1] + [8, -1, -1, -1] + [-1] * 4 + [1, 2, 3, 4]))
+    a["ring"].copy_(torch.arange(P, dtype=torch.int32, device="cuda"))
+    a["pool"].copy_(_ints([10, 12]))
+    m.moe_kv_plan(a["seq"], a["new"], R, a["table"], mb, page, a["ring"], P, a["pool"], a["so"], a["fi"], a["sl"], a["pl"], cap, a["po"],
+                  a["st"])
+    assert a["st"].tolist() == [0] and a["so"].tolist() == [9, 9, 3, 4, 32] and a["fi"].tolist() == [0, 9, 10, 10, 14, 15]
+    assert a["po"].tolist() == [14, 8]
+    assert a["sl"].tolist() == list(range(80, 89)) + [96, 104, 105, 106, 107, 39] + [-1] * 25
+    assert a["pl"].tolist() == list(range(9)) + [8, 0, 1, 2, 3, 31] + [0] * 25
+    assert a["table"].tolist() == [10, 11, -1, -1, 7, 12, -1, -1, 8, -1, -1, -1, 13, -1, -1, -1, 1, 2, 3, 4]

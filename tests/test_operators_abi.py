@@ -163,3 +163,27 @@ def test_binding_refuses_types_and_rows_it_cannot_pass_on(m):
     with pytest.raises(m.MoEError) as e:
         m.moe_paged_attention(kv, x, 3, 7, AT, AT, 4, 0.1, x, AT, stream=0)
     assert e.value.status == m.MOE_EINVAL
+
+
+# ------------------------------------------------------------ the plan's arrays
+_PLAN_R, _PLAN_MB, _PLAN_P, _PLAN_CAP = 6, 5, 40, 50
+_PLAN_ARRAYS = dict(seq=("seq_len", _PLAN_R), new=("new_len", _PLAN_R), table=("block_table", _PLAN_R * _PLAN_MB), ring=("ring", _PLAN_P),
+                    pool=("pool", 2), seq_out=("seq_out", _PLAN_R), first=("first", _PLAN_R + 1), slots=("slots", _PLAN_CAP),
+                    places=("places", _PLAN_CAP), pool_out=("pool_out", 2), status=("status", 1))
+_READ = ["seq", "new", "table", "ring", "pool"]
+_PAIRS = [(w, r) for w in ("seq_out", "first", "slots", "places", "pool_out", "status") for r in _READ]
+_PAIRS += [("ring", r) for r in ("seq", "new", "table", "pool")] + [("table", r) for r in ("seq", "new", "pool")]
+
+
+@pytest.mark.parametrize("w,r", _PAIRS)
+def test_plan_rejects_an_array_that_overlaps_what_is_read(m, w, r):
+    """All arrays apart but two: the same address, the last number of one in
+    the first place of the other, and the reverse."""
+    base = {n: AT + 4096 * i for i, n in enumerate(_PLAN_ARRAYS)}
+    nw, nr = _PLAN_ARRAYS[w][1], _PLAN_ARRAYS[r][1]
+    for at in (base[r], base[r] + 4 * (nr - 1), base[r] - 4 * (nw - 1)):
+        a = dict(base, R=_PLAN_R, mb=_PLAN_MB, P=_PLAN_P, cap=_PLAN_CAP)
+        a[w] = at
+        assert _plan(m, **a) == m.MOE_EINVAL
+        said = m.last_error()
+        assert "overlaps" in said and _PLAN_ARRAYS[w][0] in said and _PLAN_ARRAYS[r][0] in said, said
