@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanParams p) {
         if (blockIdx.x == 0)                        // (where this CTA has written its sums)
             for (int r = r0; r < r1; r++) p.seq_out[r] = p.seq[r];
         for (int r = me; r <= R; r += step) p.first[r] = 0;
-        for (int i = me; i < p.cap; i += step) {
+        for (int64_t i = me; i < p.cap; i += step) {            // (cap may be within a step of 2^31)
             p.slots[i] = -1;
             p.places[i] = 0;
         }

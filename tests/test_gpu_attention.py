@@ -589,3 +589,23 @@ def test_plan_of_arrays_that_stand_side_by_side(m):
     assert a["sl"].tolist() == list(range(80, 89)) + [96, 104, 105, 106, 107, 39] + [-1] * 25
     assert a["pl"].tolist() == list(range(9)) + [8, 0, 1, 2, 3, 31] + [0] * 25
     assert a["table"].tolist() == [10, 11, -1, -1, 7, 12, -1, -1, 8, -1, -1, -1, 13, -1, -1, -1, 1, 2, 3, 4]
+
+
+@pytest.mark.parametrize("cap", [2 ** 31 - 1, 2 ** 31 - 70000])
+def test_plan_with_room_for_all_the_slots_there_can_be(m, cap):
+    """Slots and places of almost 2^31 entries (17 GB): a step that fits and
+    one that does not, every entry written and nothing beside them."""
+    slots, places = (torch.full((cap + 2,), 9, dtype=torch.int32, device="cuda") for _ in range(2))
+    table, ring = _ints([[7, -1], [3, 5]]), torch.arange(12, dtype=torch.int32, device="cuda")
+    so, fi, po, st = (_ints([8] * n) for n in (2, 3, 2, 1))
+    for new, status, want in (([9, 2], 0, [63, 0, 1, 2, 3, 4, 5, 6, 7, 41, 42]), ([9, 9], 5, [])):
+        at = [7, 8, 9, 10, 11, 12, 13, 14, 15, 9, 10] if want else []
+        m.moe_kv_plan(_ints([7, 9]), _ints(new), 2, table, 2, 8, ring, 12, _ints([0, 4]), so, fi, slots[1:], places[1:], cap, po, st)
+        assert st.tolist() == [status]
+        for got, first, rest in ((slots, want, -1), (places, at, 0)):
+            assert got[1: 1 + len(first)].tolist() == first
+            assert int(got[0]) == 9 and int(got[-1]) == 9
+            low, high = torch.aminmax(got[1 + len(first): cap + 1])
+            assert int(low) == rest and int(high) == rest
+        slots.fill_(9)
+        places.fill_(9)
