@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxPlanRequests = 16384;     // their three sums fit shared memory
+using PlanParts = uint32_t[4][32];          // the warps' sums and flags
 
 struct PlanParams {
     const int32_t *seq, *add;
@@ -75,7 +76,7 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanParams p) {
     constexpr int WARPS = THREADS / 32;
     extern __shared__ int32_t sums[];               // [3][R + 1]
-    __shared__ uint32_t part[4][32];                // the warps' sums and flags
+    __shared__ PlanParts part;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.R;
     const int32_t *s_new = sums, *s_need = sums + R + 1, *s_gone = sums + 2 * (R + 1);
     const int page = p.page.d;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanParams p) {
 template <int THREADS>
 int launch_plan(const PlanParams &p, cudaStream_t st) {
     const size_t smem = 3 * (size_t)(p.R + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
+    if (smem + sizeof(PlanParts) > 48 * 1024) {     // (the limit is on both together)
         static OnDevices ready;
         const cudaError_t e = ready.once([] {
             return cudaFuncSetAttribute(kv_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -2,6 +2,9 @@
 plain allocator, the append against elementwise rounding, the attention of
 one new token per request against the formula in 64 bits."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -609,3 +612,28 @@ def test_plan_with_room_for_all_the_slots_there_can_be(m, cap):
             assert int(low) == rest and int(high) == rest
         slots.fill_(9)
         places.fill_(9)
+
+
+_PLAN_ALONE = """
+import sys, torch
+from int4_expert_gemv_gb300 import moe as m
+R, page, n_pages, cap = int(sys.argv[1]), 16, 20000, 5000
+i32 = lambda n, v=0: torch.full((n,), v, dtype=torch.int32, device="cuda")
+table, ring = i32(R * 2, -1), torch.arange(n_pages, dtype=torch.int32, device="cuda")
+seq, new = i32(R), i32(R, 1)
+so, fi, sl, pl, po, st = i32(R), i32(R + 1), i32(cap), i32(cap), i32(2), i32(1, 9)
+pool = torch.tensor([0, n_pages], dtype=torch.int32, device="cuda")
+m.moe_kv_plan(seq, new, R, table, 2, page, ring, n_pages, pool, so, fi, sl, pl, cap, po, st)
+at = torch.arange(R, dtype=torch.int32, device="cuda")
+assert st.tolist() == [0] and torch.equal(sl[:R], at * page) and torch.equal(table.view(R, 2)[:, 0], at)
+assert po.tolist() == [R, n_pages - R] and torch.equal(fi[:R], at) and int(fi[R]) == R and (so == 1).all()
+"""
+
+
+@pytest.mark.parametrize("R", [1024, 1025, 4010, 4052, 4053, 4095, 4096])
+def test_plan_of_any_count_is_the_first_call_of_a_process(m, R):
+    """The shared memory of a call does not go by what larger calls before it
+    have asked for: each count in a process of its own."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _PLAN_ALONE, str(R)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
