@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
         }
         m = lanes_max<LT>(m);
         const bool share = __any_sync(0xffffffffu, m == INFINITY);     // +inf logits share the mass
-        const float ref = m == INFINITY || m == -INFINITY ? 0.0f : m * 1.44269504088896341f;
+        const float ref = m == INFINITY || m == -INFINITY ? 0.0f : m;
         total = 0.0f;
 #pragma unroll
         for (int j = 0; j < SUB; j++) {
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float e = quick_exp2(fmaf(f[i], 1.44269504088896341f, -ref));
+                    // (the maximum's own term is 1 wherever the logits stand, as in the weights below)
+                    const float e = quick_exp2((f[i] - ref) * 1.44269504088896341f);
                     f[i] = f[i] > -INFINITY ? e : -FLT_MAX;            // off: -inf and NaN
                     total += fmaxf(f[i], 0.0f);
                 }

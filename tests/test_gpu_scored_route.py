@@ -175,3 +175,17 @@ def test_scored_route_equals_topk_route_and_repeats(m):
     assert np.abs(w - w2.cpu().double().numpy())[~near].max() <= 2.0 ** -19
     again = _route(m, z, 4)
     assert np.array_equal(idx, again[0]) and np.array_equal(w, again[1])
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [0.0, 100.0, -100.0, 1000.0, -1000.0, 20000.0])
+def test_scored_route_softmax_ignores_an_offset(m, offset, dt):
+    """Softmax of logits far from zero: weights that are not renormalised,
+    with and without a bias, within the same bounds."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    z = (1.5 * torch.randn((200, 256), generator=g, device="cuda") + offset).to(dt)
+    bias = 0.01 * torch.randn(256, generator=g, device="cuda")
+    n = 0
+    for kw in (dict(), dict(bias=bias), dict(n_group=8, keep=3, best=2, bias=bias)):
+        n += _check(m, z, 6, renorm=False, factor=2.5, **kw)
+    assert n >= 400                                      # of 600
