@@ -252,7 +252,12 @@ int moe_topk_route(const float *logits, int T, int E, int K, int32_t *idx,
  * A logit of -inf or NaN turns its expert off: it scores 0, its c is -inf,
  * so it comes after every expert that is on (then by index) and its weight
  * is 0; a row with nothing on gets weights 0 and valid indices.  A logit of
- * +inf has sigmoid 1, and shares softmax's whole mass with the other +inf. */
+ * +inf has sigmoid 1, and shares softmax's whole mass with the other +inf.
+ * Without a bias the choice goes by the logits, whose order the scores' is,
+ * also where fp32 does not hold the scores or tell them apart.  With a bias, c
+ * is within 2^-20 of exact (times the largest size in a row): nearer ones may
+ * stand in either order, and so may groups by the sums of two.  Scores below
+ * 2^-126 count as 0 in c. */
 typedef struct {
     int E;                    /* experts, 1 .. 1024                           */
     int K;                    /* chosen, 1 .. 16, <= keep_group * E / n_group */

@@ -80,8 +80,11 @@ __device__ __forceinline__ void logits8<__nv_bfloat16>(const void *row, int e, f
     }
 }
 
-// The choice goes by quick scores (2^-21 of exact), equal for equal logits;
-// the weights of the chosen by exact exponentials and quotients.
+// Without a bias the choice goes by the logits themselves: both scores grow
+// with them, and what fp32 cannot hold or tell apart (e^-100 beside 1, the
+// sigmoids of 20 and 21) still has its order.  With a bias it goes by quick
+// scores (2^-21 of exact, of 1; below 2^-126 they are 0), equal for equal
+// logits; the weights of the chosen by exact exponentials and quotients.
 __device__ __forceinline__ float quick_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -95,6 +98,25 @@ __device__ __forceinline__ float quick_sigmoid(float z) {
 __device__ __forceinline__ float sigmoid_f(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
 // exp(z - m), +inf logits sharing the mass.
 __device__ __forceinline__ float soft_f(float z, float m) { return z == m ? 1.0f : expf(z - m); }
+
+// The lowest choice of an expert that is on; what is off is just below it.
+constexpr float kLowest = -0x1.fffffcp127f;
+
+// A group's score by its two best logits, in an order that is the sums' also
+// where they are below fp32's numbers: the sum, or below e^-20 (where sigmoids
+// are exponentials to 2^-28) its logarithm, which is negative as no sum is.
+template <bool SIGMOID>
+__device__ __forceinline__ float pair_score(float b1, float b2, float m) {
+    if (b2 == -FLT_MAX) return b2;                  // only one is on, or none
+    if (!SIGMOID && m == INFINITY) return b1 + b2;  // (these are scores, of 0 and 1)
+    const float x1 = SIGMOID ? b1 : b1 - m, x2 = SIGMOID ? b2 : b2 - m;
+    if (x1 < -20.0f) {
+        const float sum = x1 + log1pf(expf(b2 - b1));
+        if (sum < -20.0f) return fmaxf(sum, kLowest);
+    }
+    return SIGMOID ? quick_sigmoid(x1) + quick_sigmoid(x2)
+                   : quick_exp2(x1 * 1.44269504088896341f) + quick_exp2(x2 * 1.44269504088896341f);
+}
 
 template <int LT>
 __device__ __forceinline__ float lanes_max(float v) {
@@ -157,8 +179,9 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     };
 
+    const bool raw = p.bias == nullptr;             // the choices are the logits
     float m = -INFINITY, total = 1.0f;
-    if (!SIGMOID) {                                 // the exponentials, and their sum
+    if (!SIGMOID) {                                 // the maximum
 #pragma unroll
         for (int j = 0; j < SUB; j++) {
             const int s = l + LT * j;
@@ -171,6 +194,8 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
             }
         }
         m = lanes_max<LT>(m);
+    }
+    if (!SIGMOID && !(raw && p.renorm)) {           // the exponentials, and their sum
         const bool share = __any_sync(0xffffffffu, m == INFINITY);     // +inf logits share the mass
         const float ref = m == INFINITY || m == -INFINITY ? 0.0f : m;
         total = 0.0f;
@@ -185,14 +210,18 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                     for (int i = 0; i < 8; i++)
                         if (f[i] > -INFINITY) f[i] = f[i] == INFINITY ? 0.0f : -FLT_MAX;
                 }
+                // (the maximum's own term is 1 wherever the logits stand, as in the weights below)
+                float e[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    // (the maximum's own term is 1 wherever the logits stand, as in the weights below)
-                    const float e = quick_exp2((f[i] - ref) * 1.44269504088896341f);
-                    f[i] = f[i] > -INFINITY ? e : -FLT_MAX;            // off: -inf and NaN
-                    total += fmaxf(f[i], 0.0f);
+                    e[i] = quick_exp2((f[i] - ref) * 1.44269504088896341f);
+                    total += fmaxf(e[i], 0.0f);                        // (passes NaN over)
                 }
-                put8(s, f);
+                if (!raw) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) e[i] = f[i] > -INFINITY ? e[i] : -FLT_MAX;   // off: -inf and NaN
+                    put8(s, e);
+                }
             }
         }
         total = lanes_sum<LT>(total);
@@ -208,9 +237,22 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
             // A block whose logits, and whose choices with their bias, have a
             // finite sum holds nothing that is off and no choice below -FLT_MAX:
             // one test for eight.
-            bool plain = true;
-            if (SIGMOID) {
-                read8(row, s, f);
+            bool plain = true, put = SIGMOID || p.bias || !VEC;
+            if (SIGMOID) read8(row, s, f);
+            else get8(s, f);
+            if (raw) {
+                const float z = (fabsf(f[0]) + fabsf(f[1])) + (fabsf(f[2]) + fabsf(f[3])) +
+                                ((fabsf(f[4]) + fabsf(f[5])) + (fabsf(f[6]) + fabsf(f[7])));
+                const bool share = !SIGMOID && m == INFINITY;
+                if (!(z < 0x1p127f) || share) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float c = share ? (f[i] == INFINITY ? 1.0f : 0.0f) : fmaxf(f[i], kLowest);
+                        f[i] = f[i] > -INFINITY ? c : -FLT_MAX;
+                    }
+                    put = true;
+                }
+            } else if (SIGMOID) {
                 const float z = (f[0] + f[1]) + (f[2] + f[3]) + ((f[4] + f[5]) + (f[6] + f[7]));
                 plain = fabsf(z) < INFINITY;
                 float c[8];
@@ -223,8 +265,6 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i++) f[i] = c[i];
-            } else {
-                get8(s, f);
             }
             if (p.bias) {
                 float c[8];
@@ -244,7 +284,7 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
 #pragma unroll
                 for (int i = 0; i < 8; i++) f[i] = i < n ? f[i] : -INFINITY;
             }
-            if (SIGMOID || p.bias || !VEC) put8(s, f);
+            if (put) put8(s, f);
             top[j] = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
             if (groups) {                           // the best two, by pairs
                 float hi[4], lo[4];
@@ -279,7 +319,7 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                     b2 = fmaxf(fmaxf(b2, o.y), fminf(b1, o.x));
                     b1 = fmaxf(b1, o.x);
                 }
-            score[i] = p.best == 1 ? b1 : fmaxf(b1 + b2, -FLT_MAX);
+            score[i] = p.best == 1 ? b1 : raw ? pair_score<SIGMOID>(b1, b2, m) : fmaxf(b1 + b2, -FLT_MAX);
             before[i] = 0;
         }
         uint32_t kept = 0;
@@ -355,19 +395,30 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
         __syncwarp();
     }
 
+    // Renormalised weights keep their ratios where the scores themselves are
+    // below fp32's numbers: softmax's are taken from the largest chosen logit
+    // (the sum over the row cancels), sigmoids below e^-64 as exponentials.
     constexpr int KL = (16 + LT - 1) / LT;
-    float w[KL], sum = 0.0f;
+    float z[KL], w[KL], sum = 0.0f, ref = -INFINITY;
     int e[KL];
 #pragma unroll
     for (int i = 0; i < KL; i++) {
         const int k = l + LT * i;
-        w[i] = 0.0f;
+        z[i] = -INFINITY;
         e[i] = 0;
         if (k < p.K) {
             e[i] = expert0(pick_s[k] >> 3) + (pick_s[k] & 7);
-            const float z = logit<X>(row, e[i]);
-            if (z > -INFINITY) w[i] = SIGMOID ? sigmoid_f(z) : __fdiv_rn(soft_f(z, m), total);
+            z[i] = logit<X>(row, e[i]);
         }
+        ref = fmaxf(ref, z[i]);
+    }
+    if (p.renorm) ref = lanes_max<LT>(ref);
+    if (!SIGMOID && (!p.renorm || m == INFINITY)) ref = m;
+    const bool soft = !SIGMOID || (p.renorm && ref < -64.0f);
+#pragma unroll
+    for (int i = 0; i < KL; i++) {
+        w[i] = !(z[i] > -INFINITY) ? 0.0f : soft ? soft_f(z[i], ref) : sigmoid_f(z[i]);
+        if (!SIGMOID && !p.renorm) w[i] = __fdiv_rn(w[i], total);
         sum += w[i];
     }
     sum = lanes_sum<LT>(sum);

@@ -189,3 +189,47 @@ def test_scored_route_softmax_ignores_an_offset(m, offset, dt):
     for kw in (dict(), dict(bias=bias), dict(n_group=8, keep=3, best=2, bias=bias)):
         n += _check(m, z, 6, renorm=False, factor=2.5, **kw)
     assert n >= 400                                      # of 600
+
+
+def _every_row(m, z, K, bias=None, **kw):
+    """All rows' choices equal to the rule's, whatever the margin."""
+    idx, w = _route(m, z, K, bias=bias, **kw)
+    full = dict(score="softmax", n_group=1, keep=1, best=1, renorm=True, factor=1.0)
+    full.update(kw)
+    b = None if bias is None else bias.double().cpu().numpy()
+    for t, row in enumerate(z.double().cpu().numpy()):
+        ref, rw, _ = _rule(row, K, bias=b, **full)
+        assert np.array_equal(idx[t], ref), (kw, t, idx[t], ref)
+        assert (np.abs(w[t] - rw) <= 2.0 ** -18 * np.abs(rw) + 1e-37).all(), (kw, t, w[t], rw)
+
+
+@pytest.mark.parametrize("T", [1, 6])
+def test_scored_route_without_a_bias_goes_by_the_logits(m, T):
+    """Scores that 32 bits cannot hold or tell apart (e^-100 beside 1, the
+    sigmoids of -95 and -96): the order is the logits'."""
+    E = 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    perm = torch.stack([torch.randperm(E, generator=g, device="cuda") for _ in range(T)])
+    far = (torch.arange(E, device="cuda") - 200.0)[perm]
+    far[:, 0] = 100.0                                    # one expert far above all others
+    low = (-90.0 - 0.25 * torch.arange(E, device="cuda"))[perm]
+    near = (20.0 + 0.0625 * torch.arange(E, device="cuda"))[perm]          # beside 1 by e^-20 and less
+    for z in (far, low, far.bfloat16(), low.bfloat16()):
+        for score in ("softmax", "sigmoid"):
+            _every_row(m, z, 5, score=score)
+            _every_row(m, z, 5, score=score, n_group=4, keep=2, best=1)
+            _every_row(m, z, 5, score=score, n_group=4, keep=2, best=2)
+            _every_row(m, z, 5, score=score, renorm=False, factor=2.5)
+    for z in (near, near.bfloat16()):
+        _every_row(m, z, 5, score="sigmoid")
+        _every_row(m, z, 5, score="softmax")
+
+
+def test_scored_route_equals_topk_route_of_wide_logits(m):
+    g = torch.Generator(device="cuda").manual_seed(6)
+    z = 120.0 * torch.randn((300, 256), generator=g, device="cuda")
+    idx, w = _route(m, z, 8)
+    i2, w2 = torch.empty((300, 8), dtype=torch.int32, device="cuda"), torch.empty((300, 8), device="cuda")
+    m.moe_topk_route(z, 300, 256, 8, i2, w2)
+    assert np.array_equal(idx, i2.cpu().numpy())
+    assert np.abs(w - w2.cpu().double().numpy()).max() <= 2.0 ** -19
