@@ -253,6 +253,8 @@ int moe_topk_route(const float *logits, int T, int E, int K, int32_t *idx,
  * so it comes after every expert that is on (then by index) and its weight
  * is 0; a row with nothing on gets weights 0 and valid indices.  A logit of
  * +inf has sigmoid 1, and shares softmax's whole mass with the other +inf.
+ * A logit or bias of fp32's lowest value, or a bias of -inf or NaN, does not
+ * turn its expert off: it comes last of those that are on.
  * Without a bias the choice goes by the logits, whose order the scores' is,
  * also where fp32 does not hold the scores or tell them apart.  With a bias, c
  * is within 2^-20 of exact (times the largest size in a row): nearer ones may

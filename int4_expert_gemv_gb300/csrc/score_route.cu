@@ -11,8 +11,8 @@
 // lanes: which one it was, and the largest that is left.  With 8 lanes a warp
 // does so for four tokens at once, which is what the rounds cost most of;
 // with 32 a token has the shorter chain.  Choices are floats: what is off is
-// -FLT_MAX (all other choices are kept at or above it), what is taken or
-// dropped -inf.
+// -FLT_MAX (all other choices are kept above it, at kLowest at least), what is
+// taken or dropped -inf.
 //
 // Bound.  The logits are read once (4 E bytes a token, 10.5 us for 65521
 // tokens of 256 at the copy rate) and each costs an exponential and a
@@ -101,6 +101,11 @@ __device__ __forceinline__ float soft_f(float z, float m) { return z == m ? 1.0f
 
 // The lowest choice of an expert that is on; what is off is just below it.
 constexpr float kLowest = -0x1.fffffcp127f;
+
+__device__ __forceinline__ float size8(const float *f) {
+    return (fabsf(f[0]) + fabsf(f[1])) + (fabsf(f[2]) + fabsf(f[3])) +
+           ((fabsf(f[4]) + fabsf(f[5])) + (fabsf(f[6]) + fabsf(f[7])));
+}
 
 // A group's score by its two best logits, in an order that is the sums' also
 // where they are below fp32's numbers: the sum, or below e^-20 (where sigmoids
@@ -234,17 +239,15 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
         top[j] = -INFINITY;
         if (s < p.nsub) {
             float f[8];
-            // A block whose logits, and whose choices with their bias, have a
-            // finite sum holds nothing that is off and no choice below -FLT_MAX:
-            // one test for eight.
+            // A block whose logits, and whose choices with their bias, are below
+            // 2^127 in size all together holds nothing that is off and no choice
+            // below kLowest: one test for eight.
             bool plain = true, put = SIGMOID || p.bias || !VEC;
             if (SIGMOID) read8(row, s, f);
             else get8(s, f);
             if (raw) {
-                const float z = (fabsf(f[0]) + fabsf(f[1])) + (fabsf(f[2]) + fabsf(f[3])) +
-                                ((fabsf(f[4]) + fabsf(f[5])) + (fabsf(f[6]) + fabsf(f[7])));
                 const bool share = !SIGMOID && m == INFINITY;
-                if (!(z < 0x1p127f) || share) {
+                if (!(size8(f) < 0x1p127f) || share) {
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         const float c = share ? (f[i] == INFINITY ? 1.0f : 0.0f) : fmaxf(f[i], kLowest);
@@ -253,8 +256,7 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                     put = true;
                 }
             } else if (SIGMOID) {
-                const float z = (f[0] + f[1]) + (f[2] + f[3]) + ((f[4] + f[5]) + (f[6] + f[7]));
-                plain = fabsf(z) < INFINITY;
+                plain = size8(f) < 0x1p127f;
                 float c[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) c[i] = quick_sigmoid(f[i]);
@@ -271,10 +273,9 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                 read8(p.bias, s, c);
 #pragma unroll
                 for (int i = 0; i < 8; i++) c[i] = fmaf(f[i], inv, c[i]);
-                const float z = (c[0] + c[1]) + (c[2] + c[3]) + ((c[4] + c[5]) + (c[6] + c[7]));
-                if (!plain || !(fabsf(z) < INFINITY) || !SIGMOID) {    // (softmax marks what is off by -FLT_MAX)
+                if (!plain || !(size8(c) < 0x1p127f) || !SIGMOID) {    // (softmax marks what is off by -FLT_MAX)
 #pragma unroll
-                    for (int i = 0; i < 8; i++) c[i] = f[i] == -FLT_MAX ? f[i] : fmaxf(c[i], -FLT_MAX);
+                    for (int i = 0; i < 8; i++) c[i] = f[i] == -FLT_MAX ? f[i] : fmaxf(c[i], kLowest);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i++) f[i] = c[i];
@@ -319,7 +320,10 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
                     b2 = fmaxf(fmaxf(b2, o.y), fminf(b1, o.x));
                     b1 = fmaxf(b1, o.x);
                 }
-            score[i] = p.best == 1 ? b1 : raw ? pair_score<SIGMOID>(b1, b2, m) : fmaxf(b1 + b2, -FLT_MAX);
+            score[i] = p.best == 1 ? b1
+                       : raw       ? pair_score<SIGMOID>(b1, b2, m)
+                       : b2 == -FLT_MAX ? b2
+                                        : fmaxf(b1 + b2, kLowest);
             before[i] = 0;
         }
         uint32_t kept = 0;

@@ -233,3 +233,27 @@ def test_scored_route_equals_topk_route_of_wide_logits(m):
     m.moe_topk_route(z, 300, 256, 8, i2, w2)
     assert np.array_equal(idx, i2.cpu().numpy())
     assert np.abs(w - w2.cpu().double().numpy()).max() <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scored_route_takes_the_lowest_number_before_what_is_off(m, score):
+    """A logit or a bias of the type's lowest value is a number: its expert
+    comes after all others and before those that are off."""
+    low, inf = torch.finfo(torch.float32).min, float("inf")
+    z = torch.zeros((2, 16), device="cuda")
+    z[0, :12] = -inf
+    z[0, 12:15] = low                                    # three at the lowest, one (15) above
+    z[1, :5] = float("nan")
+    z[1, 5:15] = -1.0
+    z[1, 9] = low
+    idx, w = _route(m, z, 6, score=score)
+    assert idx[0].tolist() == [15, 12, 13, 14, 0, 1]
+    assert idx[1].tolist() == [15, 5, 6, 7, 8, 10]
+    assert w[0, 0] == 1.0 and (w[0, 4:] == 0).all()
+    z = torch.zeros((1, 16), device="cuda")
+    z[0, :4] = -inf
+    bias = torch.full((16,), low, device="cuda")
+    bias[7] = 0.0
+    idx, w = _route(m, z, 14, score=score, bias=bias)
+    assert idx[0].tolist() == [7, 4, 5, 6] + list(range(8, 16)) + [0, 1]
+    assert np.abs(w[0, :12] - 1 / 12).max() <= 2.0 ** -18 and (w[0, 12:] == 0).all()
