@@ -147,8 +147,10 @@ def last_error() -> str:
 def _ptr(t):
     try:
         return t.data_ptr()
-    except AttributeError:       # None or an address
-        return t
+    except AttributeError:
+        if t is None or isinstance(t, int):      # an address
+            return t
+        raise
 
 
 _current = None

@@ -187,3 +187,17 @@ def test_plan_rejects_an_array_that_overlaps_what_is_read(m, w, r):
         assert _plan(m, **a) == m.MOE_EINVAL
         said = m.last_error()
         assert "overlaps" in said and _PLAN_ARRAYS[w][0] in said and _PLAN_ARRAYS[r][0] in said, said
+
+
+@pytest.mark.parametrize("what", [b"0123456789abcdef", "0123456789abcdef", 1.0, bytearray(16), [1, 2], object()])
+def test_binding_takes_tensors_and_addresses_and_nothing_else(m, what):
+    """ctypes would pass bytes and text on as addresses of the host."""
+    import torch
+    x, rd, kv = torch.zeros((3, 64)), _rd(m), _kv(m)
+    with pytest.raises(AttributeError):
+        m.moe_topk_route(what, 0, 64, 4, AT, AT, stream=0)
+    with pytest.raises(AttributeError):
+        m.moe_scored_route(rd, x, 0, what, AT, stream=0)
+    with pytest.raises(AttributeError):
+        m.moe_kv_append(kv, x, x, what, 0, stream=0)
+    m.moe_scored_route(rd, x, 0, None, AT, stream=0)
