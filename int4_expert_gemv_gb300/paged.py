@@ -32,9 +32,10 @@ from .model import DeviceModel
 
 class PagedCache:
     """Pages of one layer ([n_pages][2][Hkv][page][D]: a page's keys, then its
-    values) and the block tables of R requests.  plan() is one scheduler step;
-    the state it replaces (lengths, free pages) alternates between two
-    buffers, as the call does not write what it reads."""
+    values) and the block tables of R requests.  plan() is one scheduler step.
+    The call does not write what it reads (lengths, free pages), so the new
+    state is copied over the old one behind it: all addresses stay, and a
+    captured step moves on with each replay."""
 
     def __init__(self, R: int, n_pages: int, page: int, Hkv: int, D: int, max_blocks: int,
                  max_new: int, dtype=torch.bfloat16, scale: float | None = None, device="cuda"):
@@ -51,18 +52,18 @@ class PagedCache:
                                v_scale=self.scales[1].data_ptr() if e4m3 else None)
         self.table = torch.full((R, max_blocks), -1, **i32)
         self.ring = torch.arange(n_pages, **i32)
-        self.pool = [torch.tensor([0, n_pages], **i32), torch.zeros(2, **i32)]
-        self.lengths = [torch.zeros(R, **i32), torch.zeros(R, **i32)]
+        self._state, self._after = torch.zeros(R + 2, **i32), torch.zeros(R + 2, **i32)
+        self.lengths, self.pool = self._state[:R], self._state[R:]   # pool: the first free page's place, their count
+        self.pool[1] = n_pages
         self.first = torch.zeros(R + 1, **i32)
         self.slots = torch.zeros(max_new, **i32)
         self.places = torch.zeros(max_new, **i32)
         self.status = torch.zeros(1, **i32)
-        self._now = 0
 
     @property
     def seq_len(self) -> torch.Tensor:
         """Tokens of each request in the cache, those of the last plan included."""
-        return self.lengths[self._now]
+        return self.lengths
 
     def plan(self, new_len: torch.Tensor, most: int | None = None) -> None:
         """new_len int32 [R] on the device: tokens that each request adds, -1
@@ -76,11 +77,10 @@ class PagedCache:
                 or new_len.device != self.table.device):
             raise ValueError(f"new_len: int32 [{self.R}] on {self.table.device} needed, got {new_len.dtype} "
                              f"{tuple(new_len.shape)} on {new_len.device}")
-        a, b = self._now, 1 - self._now
-        moe.moe_kv_plan(self.lengths[a], new_len, self.R, self.table, self.max_blocks, self.page,
-                        self.ring, self.n_pages, self.pool[a], self.lengths[b], self.first,
-                        self.slots, self.places, most, self.pool[b], self.status)
-        self._now = b
+        moe.moe_kv_plan(self.lengths, new_len, self.R, self.table, self.max_blocks, self.page,
+                        self.ring, self.n_pages, self.pool, self._after[: self.R], self.first,
+                        self.slots, self.places, most, self._after[self.R:], self.status)
+        self._state.copy_(self._after)
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """k, v [N][Hkv * D] of the plan's new tokens, in order of requests."""
@@ -135,7 +135,8 @@ class PagedDecoder:
         """One token for each of the requests in `rows` (int64, ascending; the
         ones whose new_len is 1; at most the cache's max_new).  x fp32 [R][d]: the residual stream; the
         result is the layer's, valid in those rows.  Nothing here waits for
-        the GPU."""
+        the GPU, and a step captured in a graph can be replayed: each replay is
+        one step more."""
         ca, c, R = self.cache, self.cfg, self.cache.R
         if rows.numel() > ca.max_new:
             raise ValueError(f"{rows.numel()} tokens in a step of a cache with places for {ca.max_new}")

@@ -77,3 +77,40 @@ def test_paged_run_reports(capsys):
     from int4_expert_gemv_gb300 import paged
     r = paged.run(TINY, 3, 50, 6, Hq=4, Hkv=2, D=64)
     assert r["requests"] == 3 and r["us_per_step"] > 0 and 3 * 32 <= r["cached_tokens"] <= 3 * 56
+
+
+def test_paged_step_in_a_graph_goes_on_with_each_replay():
+    """Captured once and replayed: the same steps as without a graph, bit for
+    bit, from the lengths and free pages to the layer's result."""
+    from int4_expert_gemv_gb300 import build
+    build.build()
+    from int4_expert_gemv_gb300 import paged
+    cfg, R = replace(TINY, seed=5), 4
+    model = paged.DeviceModel(cfg, heads=False)
+    both = []
+    for _ in range(2):
+        cache = paged.PagedCache(R, 30, 4, 2, 64, 8, R)
+        both.append((cache, paged.PagedDecoder(model, cache, 4, n_group=4, keep_group=2)))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    xs = torch.randn((9, R, cfg.d), generator=g, device="cuda")
+    rows, one = torch.arange(R, device="cuda"), torch.ones(R, dtype=torch.int32, device="cuda")
+    x = xs[0].clone()
+    want = []
+    for t in range(9):
+        cache, dec = both[0]
+        out = dec.step(xs[t], rows, one).clone()
+        want.append((out, cache.seq_len.clone(), cache.pool.clone(), cache.table.clone(), cache.slots.clone(), dec.attn.clone()))
+    cache, dec = both[1]
+    dec.step(x, rows, one)                               # the first step as it is, then the graph's
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dec.step(x, rows, one)
+    for t in range(1, 9):
+        x.copy_(xs[t])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = (dec.out, cache.seq_len, cache.pool, cache.table, cache.slots, dec.attn)
+        assert cache.seq_len.tolist() == [t + 1] * R and cache.status.tolist() == [0]
+        for a, b in zip(got, want[t]):
+            assert torch.equal(a, b)

@@ -70,3 +70,22 @@ def test_a_step_of_a_cache_with_fewer_places_than_requests(paged):
     with pytest.raises(ValueError):
         dec.step(x, torch.arange(4), new)
     assert len(paged.seen) == 1
+
+
+def test_plans_go_on_from_the_same_addresses(paged, monkeypatch):
+    """What a captured plan repeats: every call reads and writes at the same
+    places, and each goes on from the last one's state."""
+    where = []
+
+    def plan(seq, new, R, table, max_blocks, page, ring, n_pages, pool, seq_out, first, slots, places, cap, pool_out, status, stream=None):
+        where.append([t.data_ptr() for t in (seq, table, ring, pool, seq_out, first, slots, places, pool_out, status)])
+        seq_out.copy_(seq + new)
+        pool_out.copy_(pool + torch.tensor([1, -1], dtype=torch.int32))
+
+    monkeypatch.setattr(paged.moe, "moe_kv_plan", plan)
+    ca = _cache(paged)
+    new = torch.arange(8, dtype=torch.int32)
+    for n in range(1, 5):
+        ca.plan(new, 3)
+        assert ca.seq_len.tolist() == [n * i for i in range(8)] and ca.pool.tolist() == [n, 20 - n]
+    assert len(where) == 4 and all(w == where[0] for w in where) and len(set(where[0])) == 10
