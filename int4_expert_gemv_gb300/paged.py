@@ -54,11 +54,13 @@ class PagedCache:
         self.ring = torch.arange(n_pages, **i32)
         self._state, self._after = torch.zeros(R + 2, **i32), torch.zeros(R + 2, **i32)
         self.lengths, self.pool = self._state[:R], self._state[R:]   # pool: the first free page's place, their count
+        self._lengths_after, self._pool_after = self._after[:R], self._after[R:]
         self.pool[1] = n_pages
         self.first = torch.zeros(R + 1, **i32)
         self.slots = torch.zeros(max_new, **i32)
         self.places = torch.zeros(max_new, **i32)
-        self.status = torch.zeros(1, **i32)
+        self.status = torch.zeros(1, **i32)          # of the last plan
+        self.worst = torch.zeros(1, **i32)           # of all plans since check()
 
     @property
     def seq_len(self) -> torch.Tensor:
@@ -69,7 +71,8 @@ class PagedCache:
         """new_len int32 [R] on the device: tokens that each request adds, -1
         for one that has ended; `most`: of all together, at most max_new (the
         places there are in `slots` and `places`, all of which the call
-        writes).  self.status tells afterwards whether it fit."""
+        writes).  A plan that does not fit changes nothing and gives no slots:
+        self.status tells, and check() for all plans since the last check."""
         most = self.max_new if most is None else most
         if not 0 <= most <= self.max_new:
             raise ValueError(f"at most {most} new tokens in a cache with places for {self.max_new}")
@@ -78,9 +81,19 @@ class PagedCache:
             raise ValueError(f"new_len: int32 [{self.R}] on {self.table.device} needed, got {new_len.dtype} "
                              f"{tuple(new_len.shape)} on {new_len.device}")
         moe.moe_kv_plan(self.lengths, new_len, self.R, self.table, self.max_blocks, self.page,
-                        self.ring, self.n_pages, self.pool, self._after[: self.R], self.first,
-                        self.slots, self.places, most, self._after[self.R:], self.status)
+                        self.ring, self.n_pages, self.pool, self._lengths_after, self.first,
+                        self.slots, self.places, most, self._pool_after, self.status)
         self._state.copy_(self._after)
+        torch.maximum(self.worst, self.status, out=self.worst)
+
+    def check(self) -> None:
+        """Waits for the GPU; raises MoEError if a plan since the last check did
+        not fit (its tokens are in no slot, and steps over it ran on the keys
+        that were there)."""
+        worst = int(self.worst[0])
+        self.worst.zero_()
+        if worst != moe.MOE_OK:
+            raise moe.MoEError(worst, "moe_kv_plan", "a step's tokens did not fit")
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """k, v [N][Hkv * D] of the plan's new tokens, in order of requests."""
@@ -136,7 +149,8 @@ class PagedDecoder:
         ones whose new_len is 1; at most the cache's max_new).  x fp32 [R][d]: the residual stream; the
         result is the layer's, valid in those rows.  Nothing here waits for
         the GPU, and a step captured in a graph can be replayed: each replay is
-        one step more."""
+        one step more.  Whether all steps' tokens had room tells the cache's
+        check(), to be asked before their results are used."""
         ca, c, R = self.cache, self.cfg, self.cache.R
         if rows.numel() > ca.max_new:
             raise ValueError(f"{rows.numel()} tokens in a step of a cache with places for {ca.max_new}")
@@ -186,8 +200,7 @@ def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int 
         x = dec.step(x, rows, one).clone()
     ev[1].record()
     torch.cuda.synchronize()
-    if int(cache.status[0]) != moe.MOE_OK:
-        raise RuntimeError(f"page plan: {moe.status_string(int(cache.status[0]))}")
+    cache.check()
     return {"requests": R, "cached_tokens": int(cache.seq_len.sum()),
             "us_per_step": ev[0].elapsed_time(ev[1]) * 1e3 / (steps - 3)}
 

@@ -114,3 +114,27 @@ def test_paged_step_in_a_graph_goes_on_with_each_replay():
         assert cache.seq_len.tolist() == [t + 1] * R and cache.status.tolist() == [0]
         for a, b in zip(got, want[t]):
             assert torch.equal(a, b)
+
+
+def test_paged_steps_without_room_are_told():
+    from int4_expert_gemv_gb300 import build
+    build.build()
+    from int4_expert_gemv_gb300 import moe, paged
+    cfg, R = replace(TINY, seed=5), 3
+    cache = paged.PagedCache(R, 3, 2, 2, 64, 8, R)       # a page of two tokens for each, and no more
+    dec = paged.PagedDecoder(paged.DeviceModel(cfg, heads=False), cache, 4, n_group=4, keep_group=2)
+    x = torch.randn((R, cfg.d), device="cuda")
+    rows = torch.arange(R, device="cuda")
+    new = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for _ in range(2):
+        dec.step(x, rows, new(1, 1, 1))
+    cache.check()
+    dec.step(x, rows, new(1, 1, 1))                      # does not fit
+    dec.step(x, rows[:0], new(0, 0, -1))                 # does
+    assert cache.status.tolist() == [0] and cache.seq_len.tolist() == [2, 2, 0]
+    with pytest.raises(moe.MoEError) as e:
+        cache.check()
+    assert e.value.status == moe.MOE_ENOSPACE
+    dec.step(x, rows[:1], new(1, 0, 0))
+    cache.check()
+    assert cache.seq_len.tolist() == [3, 2, 0]

@@ -89,3 +89,28 @@ def test_plans_go_on_from_the_same_addresses(paged, monkeypatch):
         ca.plan(new, 3)
         assert ca.seq_len.tolist() == [n * i for i in range(8)] and ca.pool.tolist() == [n, 20 - n]
     assert len(where) == 4 and all(w == where[0] for w in where) and len(set(where[0])) == 10
+
+
+def test_a_plan_that_does_not_fit_is_not_forgotten(paged, monkeypatch):
+    """Between others that do, and until it has been told once."""
+    codes = iter([0, paged.moe.MOE_ENOSPACE, 0, 0, 0, paged.moe.MOE_EINVAL])
+
+    def plan(seq, new, *a, **kw):
+        a[-1].fill_(next(codes))
+
+    monkeypatch.setattr(paged.moe, "moe_kv_plan", plan)
+    ca, new = _cache(paged), torch.zeros(8, dtype=torch.int32)
+    ca.plan(new)
+    ca.check()
+    for _ in range(3):
+        ca.plan(new)
+    assert ca.status.tolist() == [0]
+    with pytest.raises(paged.moe.MoEError) as e:
+        ca.check()
+    assert e.value.status == paged.moe.MOE_ENOSPACE
+    ca.check()
+    ca.plan(new)
+    ca.check()
+    ca.plan(new)
+    with pytest.raises(paged.moe.MoEError):
+        ca.check()
