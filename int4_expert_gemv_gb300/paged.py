@@ -177,7 +177,11 @@ class PagedDecoder:
 def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int = 2, D: int = 128,
         page: int = 16, dtype=torch.bfloat16) -> dict:
     """Requests of up to `length` cached tokens (random), `steps` decode steps
-    of one layer; times of a step and of its attention in microseconds."""
+    of one layer, the first three of them untimed where there are more; the
+    time of a step in microseconds."""
+    if steps < 1:
+        raise ValueError(f"steps={steps}")
+    timed = max(1, steps - 3)
     model = DeviceModel(cfg, heads=False)
     blocks = (length + steps + 2 * page) // page
     cache = PagedCache(R, R * blocks, page, Hkv, D, blocks, max(R, R * length), dtype, scale=0.01)
@@ -193,16 +197,16 @@ def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int 
     x = torch.randn((R, cfg.d), generator=g, device="cuda")
     rows, one = torch.arange(R, device="cuda"), torch.ones(R, dtype=torch.int32, device="cuda")
     ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
-    for _ in range(3):
+    for _ in range(steps - timed):
         dec.step(x, rows, one)
     ev[0].record()
-    for _ in range(steps - 3):
+    for _ in range(timed):
         x = dec.step(x, rows, one).clone()
     ev[1].record()
     torch.cuda.synchronize()
     cache.check()
     return {"requests": R, "cached_tokens": int(cache.seq_len.sum()),
-            "us_per_step": ev[0].elapsed_time(ev[1]) * 1e3 / (steps - 3)}
+            "us_per_step": ev[0].elapsed_time(ev[1]) * 1e3 / timed}
 
 
 if __name__ == "__main__":

@@ -138,3 +138,12 @@ def test_paged_steps_without_room_are_told():
     dec.step(x, rows[:1], new(1, 0, 0))
     cache.check()
     assert cache.seq_len.tolist() == [3, 2, 0]
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4])
+def test_paged_run_of_few_steps(steps):
+    from int4_expert_gemv_gb300 import build
+    build.build()
+    from int4_expert_gemv_gb300 import paged
+    r = paged.run(TINY, 2, 20, steps, Hq=4, Hkv=2, D=64)
+    assert r["us_per_step"] > 0 and 2 * 11 + 2 * steps <= r["cached_tokens"] <= 2 * 20 + 2 * steps

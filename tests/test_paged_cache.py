@@ -114,3 +114,9 @@ def test_a_plan_that_does_not_fit_is_not_forgotten(paged, monkeypatch):
     ca.plan(new)
     with pytest.raises(paged.moe.MoEError):
         ca.check()
+
+
+@pytest.mark.parametrize("steps", [0, -1])
+def test_run_refuses_no_steps(paged, steps):
+    with pytest.raises(ValueError):
+        paged.run(None, 1, 1, steps)
