@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
     constexpr int TOK = kRouteThreads / LT;
     const int NB = p.nsub;
     const int lane = threadIdx.x & 31, sub = threadIdx.x / LT, l = threadIdx.x % LT;
-    const int tt = blockIdx.x * TOK + sub;
-    const bool live = tt < p.T;
-    const int t = live ? tt : p.T - 1;             // the last warp's idle lanes repeat a token
+    const uint32_t tt = blockIdx.x * TOK + sub;
+    const bool live = tt < (uint32_t)p.T;
+    const int t = live ? (int)tt : p.T - 1;        // the last warp's idle lanes repeat a token
     float *c_s = smem + sub * p.tok;
     float4 *c4 = reinterpret_cast<float4 *>(c_s);
     float2 *best_s = reinterpret_cast<float2 *>(c_s + NB * 8);
@@ -447,7 +447,7 @@ int launch_sub(const RouteParams &p, cudaStream_t st) {
             [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024); });
         if (e != cudaSuccess) return fail(MOE_ECUDA, "scored_route_kernel: %s", cudaGetErrorString(e));
     }
-    kernel<<<(unsigned)((p.T + TOK - 1) / TOK), kRouteThreads, smem, st>>>(p);
+    kernel<<<((uint32_t)p.T + TOK - 1) / TOK, kRouteThreads, smem, st>>>(p);
     return check_launch("scored_route_kernel");
 }
 

@@ -257,3 +257,24 @@ def test_scored_route_takes_the_lowest_number_before_what_is_off(m, score):
     idx, w = _route(m, z, 14, score=score, bias=bias)
     assert idx[0].tolist() == [7, 4, 5, 6] + list(range(8, 16)) + [0, 1]
     assert np.abs(w[0, :12] - 1 / 12).max() <= 2.0 ** -18 and (w[0, 12:] == 0).all()
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 16])
+def test_scored_route_of_all_the_tokens_there_can_be(m, T):
+    """One or two experts: idx and w of every token, and
+    nothing behind them (21 GB and more)."""
+    E = 1 if T % 2 else 2
+    wide = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    wide.fill_(0.5)
+    if E == 2:
+        wide[::3, 1] = 0.75
+    idx = torch.full((T + 3,), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 3,), 9.0, device="cuda")
+    rd = m.RouteDesc(E=E, K=1, score=m.MOE_SCORE_SIGMOID, n_group=1, keep_group=1, group_best=1, renorm=1, factor=0.5, bias=None)
+    m.moe_scored_route(rd, wide, T, idx, w)
+    assert idx[T:].tolist() == [-9] * 3 and w[T:].tolist() == [9.0] * 3
+    for a in range(0, T, 1 << 28):
+        b = min(T, a + (1 << 28))
+        want = (torch.arange(a, b, device="cuda") % 3 == 0).int() if E == 2 else torch.zeros(b - a, dtype=torch.int32, device="cuda")
+        assert torch.equal(idx[a:b], want)
+        assert bool((w[a:b] == 0.5).all())
