@@ -421,8 +421,11 @@ __global__ void __launch_bounds__(kRouteThreads, SUB <= 4 ? 10 : 1) scored_route
     const bool soft = !SIGMOID || (p.renorm && ref < -64.0f);
 #pragma unroll
     for (int i = 0; i < KL; i++) {
-        w[i] = !(z[i] > -INFINITY) ? 0.0f : soft ? soft_f(z[i], ref) : sigmoid_f(z[i]);
-        if (!SIGMOID && !p.renorm) w[i] = __fdiv_rn(w[i], total);
+        w[i] = 0.0f;
+        if (z[i] > -INFINITY) {                     // (otherwise the row's sum may be 0 as well)
+            w[i] = soft ? soft_f(z[i], ref) : sigmoid_f(z[i]);
+            if (!SIGMOID && !p.renorm) w[i] = __fdiv_rn(w[i], total);
+        }
         sum += w[i];
     }
     sum = lanes_sum<LT>(sum);

@@ -278,3 +278,16 @@ def test_scored_route_of_all_the_tokens_there_can_be(m, T):
         want = (torch.arange(a, b, device="cuda") % 3 == 0).int() if E == 2 else torch.zeros(b - a, dtype=torch.int32, device="cuda")
         assert torch.equal(idx[a:b], want)
         assert bool((w[a:b] == 0.5).all())
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scored_route_of_rows_with_nothing_on(m, score, renorm):
+    z = torch.full((5, 40), float("-inf"), device="cuda")
+    z[1], z[2, ::2], z[3, 11] = float("nan"), float("nan"), 0.25
+    for bias in (None, torch.linspace(-1, 1, 40, device="cuda")):
+        idx, w = _route(m, z, 3, score=score, renorm=renorm, bias=bias)
+        assert idx[[0, 1, 2, 4]].tolist() == [[0, 1, 2]] * 4 and idx[3].tolist() == [11, 0, 1]
+        assert (w[[0, 1, 2, 4]] == 0).all() and (w[3, 1:] == 0).all()
+        want = 1.0 if renorm or score == "softmax" else 1 / (1 + np.exp(-0.25))
+        assert abs(w[3, 0] - want) <= 2.0 ** -18
