@@ -637,3 +637,186 @@ def test_plan_of_any_count_is_the_first_call_of_a_process(m, R):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _PLAN_ALONE, str(R)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------ calls that fill the GPU
+class _PlanAt(Plan):
+    """A plan whose slots and places begin `at` numbers behind an aligned address."""
+    at = 0
+
+    def call(self, m, new):
+        d, R, at = self.dev, self.R, self.at
+        fill = lambda n: torch.full((n,), 12345, dtype=torch.int32, device="cuda")  # noqa: E731
+        o = dict(seq=fill(R), first=fill(R + 1), slots=fill(self.cap + at + 5), places=fill(self.cap + at + 5), pool=fill(2), status=fill(1))
+        m.moe_kv_plan(d["seq"], _ints(list(new)), R, d["table"], self.mb, self.page, d["ring"], self.P, d["pool"],
+                      o["seq"], o["first"], o["slots"][at:], o["places"][at:], self.cap, o["pool"], o["status"])
+        for k in ("slots", "places"):
+            assert (o[k][:at] == 12345).all() and (o[k][at + self.cap:] == 12345).all()
+            o[k] = o[k][at: at + self.cap]
+        got = {k: v.cpu().numpy() for k, v in o.items()}
+        d["seq"], d["pool"] = o["seq"], o["pool"]
+        return got
+
+
+@pytest.mark.parametrize("at", [0, 1, 4])
+@pytest.mark.parametrize("R,max_blocks,page,n_pages,cap", [
+    (3, 4000, 16, 9000, 100003), (7, 3000, 24, 20000, 65537), (300, 60, 16, 15000, 120002), (1500, 12, 64, 14000, 400001), (2, 60000, 1, 90000, 90000)])
+def test_plan_of_prompts(m, at, R, max_blocks, page, n_pages, cap):
+    """Room for more new tokens than the grid has threads: four a thread,
+    odd counts, requests and pages that end within a thread's four."""
+    p = _PlanAt(R, max_blocks, page, n_pages, cap, seed=R + at)
+    p.at = at
+    p.upload()
+    most, seen = cap // R, []
+    for step in range(5):
+        new = p.rng.integers(0, max(2, 2 * most // 3), R)
+        new = np.where(p.rng.random(R) < 0.3, p.rng.integers(0, 4, R), new)
+        new = np.where((p.rng.random(R) < 0.2) | (p.seq + new > max_blocks * page), -1, new)
+        if step == 3:
+            new[0] = cap                                 # more than there is
+        seen.append(_same_step(m, p, new))
+    assert 0 in seen and 5 in seen
+
+
+@pytest.mark.parametrize("x", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float8_e4m3fn])
+def test_append_of_a_prompt(m, x, cache):
+    """More chunks than the grid has threads, and an odd count of tokens."""
+    N, H, page, D = 7003, 8, 24, 128
+    g = torch.Generator(device="cuda").manual_seed(N)
+    qkv = (2 * torch.randn((N, 3 * H * D + 8), generator=g, device="cuda")).to(x)
+    k, v = qkv[:, 8: 8 + H * D], qkv[:, 8 + 2 * H * D:]
+    sc = (None, None) if cache == torch.bfloat16 else tuple(0.01 + 0.01 * torch.rand(H, generator=g, device="cuda") for _ in range(2))
+    bits = torch.int16 if cache == torch.bfloat16 else torch.uint8
+    P = N // page + 9
+    kv = torch.full((P, 2, H, page, D), 77, dtype=bits, device="cuda")
+    slots = torch.randperm(P * page, generator=g, device="cuda", dtype=torch.int32)[:N].clone()
+    slots[N // 2:: 41] = -1
+    slots[3:: 97] = P * page
+    ref = kv.clone()
+    ok = (slots >= 0) & (slots < P * page)
+    at = slots[ok].long()
+    for part, (t, s) in enumerate(((k, sc[0]), (v, sc[1]))):
+        t = t[ok].reshape(-1, H, D).float()
+        if s is not None:
+            t = (t / s[:, None]).clamp(-E4M3_MAX, E4M3_MAX)
+        ref[at // page, part, :, at % page] = t.to(cache).view(bits)
+    m.moe_kv_append(_desc(m, kv, sc), k, v, slots, N)
+    assert torch.equal(kv, ref)
+
+
+def test_append_of_more_chunks_than_32_bits_count(m):
+    """4.2 million tokens of 16 heads of 256 (34 GB; keys and values are one
+    array): those around the 2^31st chunk have slots."""
+    H, D, page = 16, 256, 16
+    span = (2 ** 31 - 1) // (H * D // 8)
+    N = span + 1003
+    x = torch.empty((N, H * D), dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, span - 2, span - 1, span, span + 1, N - 2, N - 1]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for r in rows:
+        x[r] = torch.randn(H * D, generator=g, device="cuda").bfloat16()
+    slots = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    for i, r in enumerate(rows):
+        slots[r] = 3 * i + 1
+    kv = torch.zeros((3, 2, H, page, D), dtype=torch.bfloat16, device="cuda")
+    ref = kv.clone()
+    for i, r in enumerate(rows):
+        ref[(3 * i + 1) // page, :, :, (3 * i + 1) % page] = x[r].view(H, D)
+    m.moe_kv_append(_desc(m, kv), x, x, slots, N)
+    assert torch.equal(kv, ref)
+
+
+def _resident(q, cache):
+    """CTAs of heads of 128 that are on the GPU at once."""
+    two = q == torch.bfloat16 and cache == torch.bfloat16
+    return torch.cuda.get_device_properties(0).multi_processor_count * (2 if two else 3)
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+def test_attention_of_a_batch_of_one_length(m, q, cache):
+    """As many rows as there are CTAs, or a few less, of one length: the rows
+    turn out to be best left whole, and the joins have nothing to do."""
+    ctas = _resident(q, cache)
+    for lens in ([1000] * (ctas * 9 // 80), [1000] * (ctas * 9 // 80 - 2) + [0, 1], [1024] * (ctas // 8)):
+        c = _attend_case(m, lens, 32, 8, 128, 16, q, cache, seed=len(lens))
+        c["ws"].fill_(85)
+        _call(m, c)
+        _check(c)
+    n = len(lens)                                        # bad pages and lengths among them
+    c["table"][2, 5], c["table"][n - 1, 0] = c["desc"].n_pages, -1
+    c["lens"] = list(c["lens"])
+    c["lens"][4] = c["table"].shape[1] * 16 + 1
+    c["seq"][4] = c["lens"][4]
+    _call(m, c)
+    _check(c, skip=(2, 4, n - 1))
+
+
+@pytest.mark.parametrize("q,cache", TYPES)
+def test_attention_of_more_rows_than_ctas_left_whole(m, q, cache):
+    """Nearly as many long rows as CTAs and some short and empty ones, so that
+    there are more rows than CTAs but no more work than whole rows take."""
+    ctas = _resident(q, cache)
+    n = ctas * 93 // 800
+    lens = [1000] * n + [40] * (ctas // 8 - n + 3) + [0, -1]
+    c = _attend_case(m, lens, 32, 8, 128, 16, q, cache, seed=3)
+    c["ws"].fill_(85)
+    _call(m, c)
+    _check(c)
+
+
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("q,cache", TYPES)
+def test_attention_of_more_rows_than_ctas_cut(m, q, cache, page):
+    """64 ragged requests of 8 key heads, an ordinary batch: rows cut between
+    CTAs and told by the CTA of their first part; then with bad pages."""
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(1, 2500, 64)]
+    lens[7], lens[20], lens[63], lens[0] = 0, 9001, 1, 2500
+    c = _attend_case(m, lens, 32, 8, 128, page, q, cache, seed=11)
+    c["ws"].fill_(85)
+    _call(m, c)
+    _check(c)
+    want = c["o"].clone(), c["lse"].clone()
+    c["ws"].fill_(170)
+    c["out"].zero_()
+    _call(m, c)
+    assert torch.equal(c["o"], want[0]) and torch.equal(c["lse"], want[1])
+    c["window"] = 777
+    _call(m, c)
+    _check(c)
+    c["window"] = 0
+    c["table"][20, 200], c["table"][0, 3] = -1, 2 ** 31 - 1
+    _call(m, c)
+    _check(c, skip=(0, 20))
+
+
+def test_attention_of_many_rows_with_more_heads_than_a_tile(m):
+    """33 and 20 heads to a key head: tiles of 16 and a rest, more of them
+    than CTAs."""
+    for q, cache in TYPES:
+        for Hq, H, D in ((66, 2, 64), (80, 4, 128), (40, 2, 256)):
+            rng = np.random.default_rng(Hq)
+            lens = [int(n) for n in rng.integers(0, 900, 90)]
+            c = _attend_case(m, lens, Hq, H, D, 16, q, cache, seed=Hq)
+            _call(m, c)
+            _check(c)
+
+
+def test_attention_keeps_a_bad_number_to_its_own_row(m):
+    """NaN among the keys or values in sight: NaN for the heads that read it,
+    and for nobody else."""
+    for q, cache in TYPES:
+        c = _attend_case(m, [300, 40, 1200, 17], 8, 2, 64, 16, q, cache, seed=21)
+        kv = c["kv"].view(torch.int16 if cache == torch.bfloat16 else torch.uint8)
+        nan = 0x7fc0 if cache == torch.bfloat16 else 0x7f
+        kv[int(c["table"][2, 50]), 0, 1, 3, 5] = nan     # a key of request 2, key head 1
+        kv[int(c["table"][3, 1]), 1, 0, 0, 9] = nan      # a value of request 3, key head 0
+        _call(m, c)
+        assert c["o"][2, 4:].isnan().all() and c["lse"][2, 4:].isnan().all()
+        assert c["o"][3, :4, 9].isnan().all() and not c["lse"][3].isnan().any()
+        assert int(c["o"].isnan().sum()) == 4 * 64 + 4
+        clean = _attend_case(m, [300, 40, 1200, 17], 8, 2, 64, 16, q, cache, seed=21)
+        _call(m, clean)
+        ok = ~c["o"].isnan()
+        assert torch.equal(c["o"][ok], clean["o"][ok])

@@ -291,3 +291,118 @@ def test_scored_route_of_rows_with_nothing_on(m, score, renorm):
         assert (w[[0, 1, 2, 4]] == 0).all() and (w[3, 1:] == 0).all()
         want = 1.0 if renorm or score == "softmax" else 1 / (1 + np.exp(-0.25))
         assert abs(w[3, 0] - want) <= 2.0 ** -18
+
+
+def _rule_rows(z, K, score, n_group, keep, best, renorm, factor, bias):
+    """_rule for all rows at once, on the device: (idx, w, margin)."""
+    T, E = z.shape
+    z = z.double()
+    inf = float("inf")
+    on = z > -inf                                        # not -inf, not NaN
+    z0 = torch.where(on, z, -inf)
+    if score == "sigmoid":
+        s = torch.sigmoid(z0)
+    else:
+        top = z0.amax(1, keepdim=True)
+        e = torch.where(z0 == top, 1.0, torch.exp(z0 - torch.where(top.isinf(), 0.0, top)))
+        e = torch.where(on & ~((top == inf) & (z0 < inf)), e, 0.0)
+        s = e / e.sum(1, keepdim=True).clamp(min=1e-300)
+    c = torch.where(on, s + (0.0 if bias is None else bias.double()), -inf)
+    margin = torch.full((T,), inf, dtype=torch.float64, device=z.device)
+
+    def order(v, n):
+        nonlocal margin
+        o = v.sort(dim=1, descending=True, stable=True)
+        d = o.values[:, :-1] - o.values[:, 1:]
+        counts = (torch.arange(d.shape[1], device=z.device) < n) | (o.values[:, :-1] == o.values[:, n - 1: n])
+        if d.shape[1]:
+            margin = torch.minimum(margin, torch.where(counts & (d > 0) & d.isfinite(), d, inf).amin(1))
+        return o.indices[:, :n]
+
+    if keep < n_group:
+        g = c.view(T, n_group, E // n_group).sort(2, descending=True).values[:, :, :best].sum(2)
+        kept = torch.zeros((T, n_group), dtype=torch.bool, device=z.device).scatter_(1, order(g, keep), True)
+        kept = kept.repeat_interleave(E // n_group, 1)
+        # the dropped ones behind those that are off
+        key = torch.where(c == -inf, -1e300, c)
+        idx = order(torch.where(kept, key, -inf), K)
+    else:
+        idx = order(torch.where(c == -inf, -1e300, c), K)
+    w = s.gather(1, idx)
+    if renorm:
+        total = w.sum(1, keepdim=True)
+        w = torch.where(total > 0, w / total, 0.0)
+    return idx, factor * w, margin
+
+
+def _check_many(m, z, K, **kw):
+    """_check's bounds over a batch that fills the GPU."""
+    idx, w = _route(m, z, K, **kw)
+    full = dict(score="softmax", n_group=1, keep=1, best=1, renorm=True, factor=1.0, bias=None)
+    full.update(kw)
+    ref, rw, margin = (x.cpu().numpy() for x in _rule_rows(z, K, **full))
+    one = np.sort(idx, 1)
+    assert (one[:, 1:] != one[:, :-1]).all() and (one >= 0).all() and (one < z.shape[1]).all()
+    sure = margin > 2.0 ** -20
+    wrong = np.flatnonzero(sure & (idx != ref).any(1))
+    assert not len(wrong), (len(wrong), wrong[0], idx[wrong[0]], ref[wrong[0]], margin[wrong[0]])
+    off = np.flatnonzero(sure & (np.abs(w - rw) > 2.0 ** -18 * np.abs(rw) + 1e-37).any(1))
+    assert not len(off), (len(off), off[0], w[off[0]], rw[off[0]])
+    return int(sure.sum())
+
+
+MANY = 6007      # above 32 tokens an SM: eight lanes a token whatever the width; a part of a block and of a warp at the end
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,n_group,keep,best", SHAPES + [(1023, 16, 31, 9, 2), (640, 12, 32, 11, 1), (1024, 1, 16, 16, 1)])
+def test_scored_route_of_many_tokens(m, score, E, K, n_group, keep, best):
+    g = torch.Generator(device="cuda").manual_seed(E * 31 + K)
+    z = 1.5 * torch.randn((MANY, E), generator=g, device="cuda")
+    z[::7, E // 2:] = z[::7, : E - E // 2]               # equal logits
+    z[5::11, : max(0, E // 3)] = float("-inf")
+    z[6::13, E - E // 4:] = float("nan")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    kw = dict(score=score, n_group=n_group, keep=keep, best=best)
+    n = 0
+    for x in (z, z.bfloat16()):
+        n += _check_many(m, x, K, **kw)
+        n += _check_many(m, x, K, bias=bias, renorm=False, factor=2.5, **kw)
+    assert n >= 0.7 * 4 * MANY
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scored_route_of_many_tokens_answers_as_of_few(m, score):
+    """Rows of ties, infinities, NaN, lowest numbers and far logits: the same
+    choices in a batch that fills the GPU as in one of a few tokens."""
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
+    g = torch.Generator(device="cuda").manual_seed(9)
+    z = torch.randn((16, 96), generator=g, device="cuda")
+    z[0], z[1], z[2, ::2], z[3] = 0.0, -inf, nan, nan
+    z[4, 7], z[4, 50] = inf, inf
+    z[5, :90], z[6, 1:], z[7, ::3] = low, -inf, -inf
+    z[7, 1::3] = low
+    z[8] = torch.arange(96, device="cuda") - 300.0
+    z[8, 0] = 200.0
+    z[9] = -90.0 - 0.5 * torch.arange(96, device="cuda")
+    z[10] = 30.0 + torch.arange(96, device="cuda")
+    z[11, 40:], z[12, 8:16], z[12, 20] = 5.0, nan, inf
+    many = z.repeat(400, 1)
+    bias = 0.25 * torch.randn(96, generator=g, device="cuda")
+    bias[::5] = low
+    for kw in (dict(), dict(n_group=12, keep=3, best=2), dict(n_group=4, keep=2, best=1), dict(n_group=32, keep=5, best=2)):
+        for b in (None, bias):
+            for renorm in (True, False):
+                a = _route(m, z, 6, score=score, bias=b, renorm=renorm, **kw)
+                c = _route(m, many, 6, score=score, bias=b, renorm=renorm, **kw)
+                assert np.array_equal(np.tile(a[0], (400, 1)), c[0])
+                # sums over a row in another order: 96 terms in fp32
+                assert (np.abs(np.tile(a[1], (400, 1)) - c[1]) <= 2.0 ** -19 * np.abs(c[1])).all()
+
+
+def test_scored_route_of_many_rows_of_a_wider_tensor(m):
+    g = torch.Generator(device="cuda").manual_seed(12)
+    for dt in (torch.float32, torch.bfloat16):
+        wide = torch.randn((MANY, 131), generator=g, device="cuda").to(dt)
+        for kw in (dict(n_group=4, keep=2, best=2), dict(n_group=12, keep=5, best=2), dict()):
+            assert _check_many(m, wide[:, 3:63], 4, score="sigmoid", **kw) > 0.7 * MANY
