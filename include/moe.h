@@ -293,7 +293,7 @@ typedef struct {
     int dtype;                /* MOE_DTYPE_BF16 or MOE_DTYPE_E4M3             */
     void *k, *v;              /* 16-byte aligned                              */
     size_t page_stride;       /* bytes, a multiple of 16, >= Hkv * page * D
-                                 numbers                                      */
+                                 numbers; the attention takes up to 2^32 - 1  */
     const float *k_scale;     /* E4M3: [Hkv] fp32 on the device, or NULL (1)  */
     const float *v_scale;
 } moe_kv_desc;
@@ -342,11 +342,16 @@ int moe_kv_append(const moe_kv_desc *kv, const void *k, size_t k_stride, const v
  *   x_i = scale * q . k_i,  i over the last min(len, window) of the request's
  *   len = seq_len[b] tokens (window 0: all);  out = sum softmax(x)_i v_i,
  *   lse = log sum exp(x_i)  (natural; lets parts over other keys be joined).
+ * scale is finite and above 0; B and Hq are at most 65536, Hq is a multiple of
+ * Hkv and B * Hq below 2^31; page_stride is below 2^32.
  * Query head h reads key head h / (Hq / Hkv).  q and out [B][Hq][D] in
  * q_dtype (F32 or BF16), rows q_stride / out_stride elements apart (16-byte
  * multiples); lse fp32 [B][Hq], or NULL.  block_table [B][max_blocks].
  * A request of length <= 0 has out 0 and lse -inf.  Whatever stands in the
- * cache behind a request's length is without effect.  A page id outside
+ * cache behind a request's length, or in front of its window, is without
+ * effect.  NaN in sight, and infinities where their products are (numbers that
+ * go in parts meet an infinity as inf - inf), give NaN to the heads that read
+ * them and to no others.  A page id outside
  * [0, n_pages), or a length above max_blocks * page (or 2^31 - 2^16), is never
  * read through: that request's out and lse are NaN.
  * Scores, statistics and sums in fp32; products on the tensor cores from

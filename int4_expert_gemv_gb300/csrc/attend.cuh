@@ -13,8 +13,9 @@
 //
 // What bounds it: the cache's bytes.  Measured on one GB300, of the copy rate
 // (6768 GB/s): two requests of 130977 tokens, 8 heads to a key head of 128,
-// bf16 162 us (98 %); 64 ragged ones of up to 8192, 4 heads, 146 us (95 %); 96
-// of up to 16384 over an e4m3 cache 236 us (93 %).  Small calls are bound by
+// bf16 161 us (99 %); 64 ragged ones of up to 8192, 4 heads, 143 us (97 %; 151
+// with an fp32 q); 96 of up to 16384 over an e4m3 cache 231 us (95 %; 234 with
+// an fp32 q).  Small calls are bound by
 // their launches and one chain of loads (length, table, keys), fp32 q by a
 // tile's own latencies (29 windows of 1000, heads of 80: 25 us, 52 %).  A
 // key or value number is used by G heads, 2 G flops for 2 bytes (bf16): far

@@ -17,14 +17,17 @@
 // Bound.  The logits are read once (4 E bytes a token, 10.5 us for 65521
 // tokens of 256 at the copy rate) and each costs an exponential and a
 // reciprocal for its sigmoid: 16 of those a clock and SM make 7 us there.
-// Measured 32 us with bias and 4 of 8 groups, K = 8: issue slots (64 % taken)
-// and the latencies of shared memory and shuffles share it; a round costs 1.4
-// us, the groups 3.5, the bias 2, and the rest 17.  A warp per token with a
-// warp-wide integer maximum per round took 68 us; two or four lanes a token 41
-// (shared memory then halves the warps of an SM); the lane of a block going
-// through its eight alone 35; a block's second choice kept in a register 36,
-// and 64 instead of 45 with K = 16 (some token of the four always has to look
-// for a third); the row asked for ahead into L2 33.
+// Measured 31.0 us with bias and 4 of 8 groups, K = 8: issue slots (68 % taken)
+// and the latencies of shared memory and shuffles share it; a round costs 1.2
+// us (1.5 past the eighth), the groups 3.8, and the rest 17: loads, scores, the
+// way of all choices through shared memory, weights.  Without a bias the
+// choices are the logits: 25.0 us without groups (softmax 24.4), 30.5 with
+// groups by their best two.  Beside the 32 us of an earlier state, a warp per
+// token with a warp-wide integer maximum per round took 68; two or four lanes a
+// token 41 (shared memory then halves the warps of an SM); the lane of a block
+// going through its eight alone 35; a block's second choice kept in a register
+// 36, and 64 instead of 45 with K = 16 (some token of the four always has to
+// look for a third); the row asked for ahead into L2 33.
 #include <cfloat>
 #include <type_traits>
 
@@ -475,9 +478,9 @@ int launch_lt(const RouteParams &p, cudaStream_t st) {
 template <typename X, bool SIGMOID>
 int launch_route(const RouteParams &p, cudaStream_t st) {
     // 32 lanes a token while that does not fill the SMs.  Measured, 32 against
-    // 8 lanes (tokens x experts): 1 x 256 3.7 / 5.7 us, 2525 x 160 5.2 / 5.5,
-    // 4096 x 512 5.3 / 6.5, but 4433 x 60 5.4 / 3.2, 9028 x 64 9.1 / 3.8,
-    // 65521 x 256 80 / 35.
+    // 8 lanes (tokens x experts): 1 x 256 3.8 / 5.5 us, 1216 x 128 4.6 / 4.8,
+    // 2525 x 160 6.1 / 6.8, 4096 x 512 4.4 / 6.3, but 4433 x 60 4.3 / 3.1, 9028 x
+    // 64 6.1 / 3.2, 8000 x 512 7.1 / 6.7, 65521 x 256 66 / 31.
     const int most = num_sms() * (p.nsub > 16 ? 32 : 8);
     return p.T <= most ? launch_lt<X, SIGMOID, 32>(p, st) : launch_lt<X, SIGMOID, 8>(p, st);
 }
