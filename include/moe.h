@@ -256,7 +256,8 @@ int moe_topk_route(const float *logits, int T, int E, int K, int32_t *idx,
  * A logit or bias of fp32's lowest value, or a bias of -inf or NaN, does not
  * turn its expert off: it comes last of those that are on.
  * Without a bias the choice goes by the logits, whose order the scores' is,
- * also where fp32 does not hold the scores or tell them apart.  With a bias, c
+ * also where fp32 does not hold the scores or tell them apart (beside a logit
+ * of +inf softmax's finite ones all score 0, and go by index).  With a bias, c
  * is within 2^-20 of exact (times the largest size in a row): nearer ones may
  * stand in either order, and so may groups by the sums of two.  Scores below
  * 2^-126 count as 0 in c. */
