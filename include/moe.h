@@ -47,7 +47,11 @@
  * slots and free pages of a scheduler step), moe_kv_append (keys and values
  * into a paged cache), moe_paged_attention (one new token of each request
  * over the cache) and moe_scored_route (routing by softmax or sigmoid scores
- * with a balance bias and groups).
+ * with a balance bias and groups).  Its dense half in 8-bit floating point:
+ * moe_add_rms_norm (the residual's addition, the norm, the next product's
+ * input), moe_quantise_e4m3, moe_scaled_product (a matrix product with a scale
+ * for each block of 128) and moe_rotary (queries and keys turned by their
+ * places).
  *
  * Conventions shared by every call
  *  - Memory: every pointer argument is a DEVICE pointer unless stated
@@ -115,13 +119,31 @@ const char *moe_last_error(void);
 enum {
     MOE_DTYPE_F32 = 0,      /* activations in fp32                             */
     MOE_DTYPE_BF16 = 1,     /* activations in bfloat16; a key-value cache too  */
-    MOE_DTYPE_E4M3 = 2      /* a key-value cache in 8-bit floating point (4
+    MOE_DTYPE_E4M3 = 2      /* a key-value cache, or numbers with a scale for
+                               each block, in 8-bit floating point (4
                                exponent, 3 mantissa bits, no infinity)         */
 };
 
 enum {
     MOE_SCORE_SOFTMAX = 0,  /* an expert's score: softmax over all E logits    */
     MOE_SCORE_SIGMOID = 1   /* or the sigmoid of its own logit                 */
+};
+
+enum {
+    MOE_ROTARY_HALF = 0,        /* pairs (i, i + rot / 2)                      */
+    MOE_ROTARY_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1)                        */
+};
+
+enum {                          /* how frequencies f_i = base^(-2 i / rot) are
+                                   scaled for long contexts                    */
+    MOE_ROTARY_PLAIN = 0,       /* not                                         */
+    MOE_ROTARY_LINEAR = 1,      /* f / factor                                  */
+    MOE_ROTARY_BASE = 2,        /* base * factor^(rot / (rot - 2)) as the base */
+    MOE_ROTARY_YARN = 3,        /* f for pairs that turn more than `high` times
+                                   within `trained` places, f / factor for
+                                   those that turn less than `low` times,
+                                   between them a ramp over the pairs          */
+    MOE_ROTARY_BANDS = 4        /* the same with a ramp over the turns         */
 };
 
 enum {
@@ -367,6 +389,109 @@ int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_dtype, size_
                         int B, int Hq, const int32_t *seq_len, const int32_t *block_table,
                         int max_blocks, float scale, int window, void *out, size_t out_stride,
                         float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- dense */
+/* Numbers in 8 bits with a scale for each block: a matrix [rows][cols] of e4m3
+ * codes, and of each block of 128 columns (the last one of a row may be
+ * shorter) and 1 or 128 rows a scale; a code stands for itself times its
+ * block's scale.  Scales are fp32, [ceil(rows / block_rows)][ceil(cols / 128)],
+ * rows scale_stride elements apart.  Quantised here:
+ *   scale = max(largest size in the block / 448, 2^-100), with pow2 the next
+ *   power of two that is not below it;  code = e4m3(x / scale), the quotient
+ *   rounded to fp32 and then to nearest even.
+ * A block with NaN or an infinity has a NaN scale and NaN codes. */
+
+/* x [rows][cols] (F32 or BF16) by blocks of block_rows (1: activations, 128:
+ * weights) x 128.  Rows x_stride / code_stride elements apart (16-byte
+ * multiples; anything for a single row); at most 2^31 - 1 spans of 256 columns,
+ * and 65535 * 128 rows with block_rows 128.  Outputs overlap nothing. */
+int moe_quantise_e4m3(const void *x, int x_dtype, size_t x_stride, int rows, int cols,
+                      int block_rows, int pow2, void *codes, size_t code_stride, float *scales,
+                      size_t scale_stride, cudaStream_t stream);
+
+typedef struct {
+    int d;                    /* numbers of a row, 1 .. 32768                 */
+    float eps;                /* finite, not negative                         */
+    const void *weight;       /* [d], or NULL (one)                           */
+    int w_dtype;              /* MOE_DTYPE_F32 or MOE_DTYPE_BF16              */
+    int pow2;                 /* an E4M3 result's scales are powers of two    */
+} moe_norm_desc;
+
+/* For each of T rows, in fp32:  h = x + res;  sum = h;
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * x and res [T][d] F32 or BF16 (each its own), res NULL: h = x.  sum [T][d] in
+ * res's type, or NULL.  y [T][d] in y_dtype F32, BF16 or E4M3; y comes from h
+ * before sum is rounded, and is rounded once.  E4M3: codes and the scales of
+ * 1 x 128 blocks (scales is read for no other type).  Rows x_stride, ...
+ * elements apart, 16-byte multiples (anything for T = 1).  The squares' sum is
+ * fp32: rows of numbers above 2^63 overflow it.  A row with NaN is NaN.
+ * sum and y may be x or res themselves (the same address, type and stride);
+ * no other overlap of an output. */
+int moe_add_rms_norm(const moe_norm_desc *nd, const void *x, int x_dtype, size_t x_stride,
+                     const void *res, int res_dtype, size_t res_stride, int T, void *sum,
+                     size_t sum_stride, void *y, int y_dtype, size_t y_stride, float *scales,
+                     size_t scale_stride, cudaStream_t stream);
+
+/* A weight matrix [N][K] of e4m3 codes with scales of 128 x 128 blocks. */
+typedef struct {
+    int N, K;                 /* rows (outputs), columns (inputs)             */
+    const void *w;            /* codes, 16-byte aligned                       */
+    size_t w_stride;          /* bytes between rows, a multiple of 16, >= K   */
+    const float *scales;      /* [ceil(N / 128)][ceil(K / 128)]               */
+    size_t scale_stride;      /* elements between its rows                    */
+} moe_scaled_matrix_desc;
+
+/* out [T][N] = x W^T:  out[t][n] = sum over blocks b of 128 columns of
+ *   (x_scales[t][b] * W.scales[n / 128][b]) * sum_{k in b} x[t][k] W[n][k]
+ * x: e4m3 codes [T][K] with scales of 1 x 128 blocks (moe_quantise_e4m3 or
+ * moe_add_rms_norm makes them), rows x_stride bytes apart (a multiple of 16).
+ * out: F32 or BF16, rows out_stride elements apart (16-byte multiples).  The
+ * products of codes are exact, sums are fp32, and so is the product of two
+ * scales; a block's sum, in the tensor cores, meets its scales before the next
+ * block's.  The same inputs give the same bits on the same device.
+ * ws: moe_scaled_product_workspace_bytes() bytes, 256-byte aligned, ZEROED
+ * before its first call (never again, unless a call reports an error): int32
+ * word 0 is MOE_OK, or MOE_ETIMEOUT once a bounded device-side wait of any call
+ * on it has expired (that call's outputs are invalid).  Calls at the same time
+ * may share it. */
+size_t moe_scaled_product_workspace_bytes(const moe_scaled_matrix_desc *wd, int T);
+int moe_scaled_product(const moe_scaled_matrix_desc *wd, const void *x, size_t x_stride,
+                       const float *x_scales, size_t x_scale_stride, int T, void *out,
+                       int out_dtype, size_t out_stride, void *ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/* Rotary embedding.  Of each head's D numbers the part first .. first + rot - 1
+ * turns, in pairs (a, b) of frequency f_i:  with the angle place * f_i
+ *   a' = amplitude (a cos - b sin),  b' = amplitude (b cos + a sin). */
+typedef struct {
+    int D;                    /* head size, 2 .. 1024                         */
+    int rot;                  /* numbers that turn, even                      */
+    int first;                /* the first of them; first + rot <= D          */
+    int layout;               /* MOE_ROTARY_HALF or MOE_ROTARY_INTERLEAVED    */
+    int scaling;              /* MOE_ROTARY_PLAIN ...                         */
+    int trained;              /* YARN, BANDS: places the model has been
+                                 trained on                                   */
+    double base;              /* above 1                                      */
+    double factor;            /* 1 .. 10^6 (not for PLAIN)                    */
+    double low, high;         /* YARN, BANDS: turns, 0 < low < high           */
+    float amplitude;          /* finite                                       */
+} moe_rotary_desc;
+
+/* turns [rot / 2] (device, 8-byte aligned): the frequencies, as the 64 bits
+ * behind the point of the turns a place.  Made once. */
+int moe_rotary_table(const moe_rotary_desc *rd, uint64_t *turns, cudaStream_t stream);
+
+/* Turns Hq heads of q and Hk heads of k (either may be 0, its pointers NULL) of
+ * T tokens at places[t] (int32, any).  q, k, q_out, k_out: [T][H][D] in dtype
+ * (F32 or BF16), a token's heads next to each other, tokens *_stride elements
+ * apart, aligned to their numbers (16-byte boundaries are faster).  Angles are
+ * exact to 2^-52 of a turn times the place; cosines, sines and products fp32.
+ * Out of place the numbers that do not turn are copied.  q_out may be q and
+ * k_out may be k (the same address and stride); no other overlap of an output. */
+int moe_rotary(const moe_rotary_desc *rd, const uint64_t *turns, const int32_t *places, int T,
+               int dtype, const void *q, size_t q_stride, int Hq, void *q_out,
+               size_t q_out_stride, const void *k, size_t k_stride, int Hk, void *k_out,
+               size_t k_out_stride, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- experts */
 typedef struct {

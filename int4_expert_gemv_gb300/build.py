@@ -26,7 +26,8 @@ LIBS = {
     "libmoe.so": ["abi.cu", "pack.cu", "ffn.cu", "grouped.cu", "head_route.cu", "noalloc.cu",
                   "step.cu", "chain.cu", "lora_merge.cu", "gather.cu",
                   "kv.cu", "attend.cu", "attend_bf16_qf32.cu", "attend_bf16_qbf16.cu",
-                  "attend_e4m3_qf32.cu", "attend_e4m3_qbf16.cu", "score_route.cu"],
+                  "attend_e4m3_qf32.cu", "attend_e4m3_qbf16.cu", "score_route.cu", "norm_quant.cu", "rotary.cu",
+                  "scaled_product.cu"],
     "libmoe_synth.so": ["synth.cu"],
 }
 

@@ -17,8 +17,7 @@
 // under a profiler, 52 % of the issue slots taken, next to nothing from DRAM.
 #include <algorithm>
 
-#include <cuda_fp8.h>
-
+#include "e4m3.cuh"
 #include "fastdiv.cuh"
 #include "internal.h"
 
@@ -259,73 +258,10 @@ struct AppendParams {
     const float *k_scale, *v_scale;
 };
 
-struct Floats8 {
-    float x[8];
-};
-template <typename X>
-__device__ __forceinline__ Floats8 floats8(const uint4 *raw) {
-    const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
-    Floats8 f;
-    if (sizeof(X) == 2) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f.x[2 * j] = __uint_as_float(w[j] << 16);
-            f.x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-    } else {
-        const uint4 hi = raw[sizeof(X) / 2 - 1];
-        const uint32_t z[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f.x[j] = __uint_as_float(w[j]);
-            f.x[4 + j] = __uint_as_float(z[j]);
-        }
-    }
-    return f;
-}
-
-// Eight numbers stored as bf16, rounded to nearest even.
-__device__ __forceinline__ void store8_bf16(uint8_t *dst, const float *f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight e4m3 numbers of f scaled by `by`.
-__device__ __forceinline__ uint2 e4m3x8(const float *f, float by) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        w[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * by, f[2 * j + 1] * by), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
-}
-
-// The stored number is x / scale rounded to fp32 and then to e4m3.  Rounding is
-// monotone, and x times 1 / scale (1 - 2^-21) and x times 1 / scale (1 + 2^-21) lie
-// below and above that quotient (their own roundings move them by 3 2^-24,
-// the quotient's by 2^-24; neither scale nor its reciprocal is subnormal or
-// infinite): where both give one e4m3 number, it is the quotient's, and eight
-// numbers need a division once in some 15,000.  (65521 tokens of 8 heads of 128
-// from fp32: 116 us dividing all, 107 this way; from bf16 84 and 77.)
+// (65521 tokens of 8 heads of 128 from fp32: 116 us dividing all, 107 with the
+// division left to where two products differ; from bf16 84 and 77.)
 __device__ __forceinline__ void store8_e4m3(uint8_t *dst, const float *f, float scale, float2 inv) {
-    uint2 w = e4m3x8(f, inv.x);
-    const uint2 up = e4m3x8(f, inv.y);
-    if (w.x != up.x || w.y != up.y || !(fabsf(scale) > 0x1p-125f && fabsf(scale) < 0x1p125f)) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = __fdiv_rn(f[j], scale);
-        w = e4m3x8(y, 1.0f);
-    }
-    *reinterpret_cast<uint2 *>(dst) = w;
-}
-
-__device__ __forceinline__ float2 inverses(float scale) {
-    const float inv = __fdiv_rn(1.0f, scale);
-    return make_float2(inv * (1.0f - 0x1p-21f), inv * (1.0f + 0x1p-21f));
+    *reinterpret_cast<uint2 *>(dst) = e4m3_quotients(f, scale, inv);
 }
 
 // One thread takes 8 keys and 8 values of a token: 16-byte loads, neighbours in

@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECUDA, MOE_ETIMEOUT, MOE_ENOSPACE = range(6)
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_E4M3 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ROTARY_HALF, MOE_ROTARY_INTERLEAVED = 0, 1
+MOE_ROTARY_PLAIN, MOE_ROTARY_LINEAR, MOE_ROTARY_BASE, MOE_ROTARY_YARN, MOE_ROTARY_BANDS = range(5)
 MOE_PREC_AFFINE4, MOE_PREC_FP16 = 4, 16
 
 _lock = threading.Lock()
@@ -78,6 +80,23 @@ class KVDesc(C.Structure):
                 ("page_stride", C.c_size_t), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
 
 
+class NormDesc(C.Structure):
+    _fields_ = [("d", C.c_int), ("eps", C.c_float), ("weight", C.c_void_p), ("w_dtype", C.c_int),
+                ("pow2", C.c_int)]
+
+
+class ScaledMatrixDesc(C.Structure):
+    _fields_ = [("N", C.c_int), ("K", C.c_int), ("w", C.c_void_p), ("w_stride", C.c_size_t),
+                ("scales", C.c_void_p), ("scale_stride", C.c_size_t)]
+
+
+class RotaryDesc(C.Structure):
+    _fields_ = [("D", C.c_int), ("rot", C.c_int), ("first", C.c_int), ("layout", C.c_int),
+                ("scaling", C.c_int), ("trained", C.c_int), ("base", C.c_double),
+                ("factor", C.c_double), ("low", C.c_double), ("high", C.c_double),
+                ("amplitude", C.c_float)]
+
+
 # ------------------------------------------------------------------ loading
 def lib():
     global _lib
@@ -114,6 +133,15 @@ def lib():
                 "moe_paged_attention_workspace_bytes": (S, [C.POINTER(KVDesc), I, I]),
                 "moe_paged_attention": (I, [C.POINTER(KVDesc), P, I, S, I, I, P, P, I, C.c_float, I,
                                             P, S, P, P, S, P]),
+                "moe_quantise_e4m3": (I, [P, I, S, I, I, I, I, P, S, P, S, P]),
+                "moe_add_rms_norm": (I, [C.POINTER(NormDesc), P, I, S, P, I, S, I, P, S, P, I, S,
+                                         P, S, P]),
+                "moe_scaled_product_workspace_bytes": (S, [C.POINTER(ScaledMatrixDesc), I]),
+                "moe_scaled_product": (I, [C.POINTER(ScaledMatrixDesc), P, S, P, S, I, P, I, S, P,
+                                           S, P]),
+                "moe_rotary_table": (I, [C.POINTER(RotaryDesc), P, P]),
+                "moe_rotary": (I, [C.POINTER(RotaryDesc), P, P, I, I, P, S, I, P, S, P, S, I, P, S,
+                                   P]),
                 "moe_expert_ffn_workspace_bytes": (S, [C.POINTER(ExpertsDesc), I, I]),
                 "moe_expert_ffn_int4": (I, [C.POINTER(ExpertsDesc), P, I, P, I, I, P, P, S, P]),
                 "moe_combine_residual": (I, [P, P, I, I, I, I, P, P, P, P]),
@@ -354,6 +382,84 @@ def moe_paged_attention(kv: KVDesc, q, B: int, Hq: int, seq_len, block_table, ma
                                      _ptr(seq_len), _ptr(block_table), max_blocks, scale, window,
                                      _ptr(out), _row_stride(out), _ptr(lse), _ptr(ws), _nbytes(ws),
                                      _stream(stream)), "moe_paged_attention")
+
+
+def _codes_dtype(t) -> int:
+    """The type of a result that may be in 8 bits."""
+    import torch
+    return MOE_DTYPE_E4M3 if t.dtype in (torch.float8_e4m3fn, torch.uint8) else _dtype_code(t)
+
+
+def _code_rows(t, what: str) -> int:
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{what} must be float8_e4m3fn (or uint8), got {t.dtype}")
+    return _row_stride(t)
+
+
+def _f32(t, what: str):
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32, got {t.dtype}")
+    return _row_stride(t)
+
+
+def moe_quantise_e4m3(x, rows: int, cols: int, codes, scales, block_rows: int = 1,
+                      pow2: bool = False, stream=None):
+    """x fp32 or bf16 [rows][cols] as e4m3 codes with a fp32 scale for each
+    block of block_rows (1 or 128) x 128; rows may be strided."""
+    _check(lib().moe_quantise_e4m3(_ptr(x), _dtype_code(x), _row_stride(x), rows, cols, block_rows,
+                                   int(bool(pow2)), _ptr(codes), _code_rows(codes, "codes"),
+                                   _ptr(scales), _f32(scales, "scales"), _stream(stream)),
+           "moe_quantise_e4m3")
+
+
+def moe_add_rms_norm(nd: NormDesc, x, T: int, y, res=None, sum=None, scales=None, stream=None):
+    """y = h / sqrt(mean(h^2) + eps) * weight of h = x + res (res None: x), and
+    h itself into sum (of res's type; may be res).  y fp32, bf16 or e4m3 codes
+    with their scales; rows may be strided."""
+    yd = _codes_dtype(y)
+    if sum is not None and res is not None and sum.dtype != res.dtype:
+        raise TypeError(f"sum and res must have one type, got {sum.dtype} and {res.dtype}")
+    _check(lib().moe_add_rms_norm(
+        C.byref(nd), _ptr(x), _dtype_code(x), _row_stride(x), _ptr(res),
+        MOE_DTYPE_F32 if res is None else _dtype_code(res), 0 if res is None else _row_stride(res),
+        T, _ptr(sum), 0 if sum is None else _row_stride(sum), _ptr(y), yd, _row_stride(y),
+        _ptr(scales), 0 if scales is None else _f32(scales, "scales"), _stream(stream)),
+        "moe_add_rms_norm")
+
+
+def moe_scaled_product_workspace_bytes(wd: ScaledMatrixDesc, T: int) -> int:
+    return lib().moe_scaled_product_workspace_bytes(C.byref(wd), T)
+
+
+def moe_scaled_product(wd: ScaledMatrixDesc, x, x_scales, T: int, out, ws, stream=None):
+    """out [T][N] (fp32 or bf16) = x W^T of e4m3 codes x [T][K] with scales for
+    each 128 of a row; ws: zeroed once, its word 0 is the status."""
+    _check(lib().moe_scaled_product(C.byref(wd), _ptr(x), _code_rows(x, "x"), _ptr(x_scales),
+                                    _f32(x_scales, "x_scales"), T, _ptr(out), _dtype_code(out),
+                                    _row_stride(out), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "moe_scaled_product")
+
+
+def moe_rotary_table(rd: RotaryDesc, turns, stream=None):
+    """The frequencies of a rotary embedding, int64 (or uint64) [rot / 2]."""
+    _check(lib().moe_rotary_table(C.byref(rd), _ptr(turns), _stream(stream)), "moe_rotary_table")
+
+
+def moe_rotary(rd: RotaryDesc, turns, places, T: int, q, Hq: int, q_out, k=None, Hk: int = 0,
+               k_out=None, stream=None):
+    """q and k, [T][H][D] or [T][H * D], fp32 or bf16, turned by their places
+    (int32 [T]) into q_out and k_out, which may be q and k; tokens may be
+    strided."""
+    one = q if q is not None else k
+    for t in (q, q_out, k, k_out):
+        if t is not None and t.dtype != one.dtype:
+            raise TypeError(f"q, k and their results must have one type, got {one.dtype} and {t.dtype}")
+    row = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
+    _check(lib().moe_rotary(C.byref(rd), _ptr(turns), _ptr(places), T, _dtype_code(one), _ptr(q),
+                            row(q), Hq, _ptr(q_out), row(q_out), _ptr(k), row(k), Hk, _ptr(k_out),
+                            row(k_out), _stream(stream)), "moe_rotary")
 
 
 def moe_expert_ffn_int4(ed: ExpertsDesc, x, idx, T: int, K: int, y_slots, ws, stream=None,
