@@ -9,6 +9,7 @@
 // block's two scales.  Nothing but the inner sum of 128 is left to the tensor
 // cores, and any fp32 scale is met exactly.
 #include <algorithm>
+#include <cstdlib>
 
 #include "e4m3.cuh"
 #include "gemm_umma.cuh"
@@ -28,7 +29,6 @@ using pipe::saddr;
 using umma::sw128_desc;
 using umma::tc_fence_after;
 using umma::tc_fence_before;
-using umma::uwait;
 
 struct ProductParams {
     const float *sx, *sw;
@@ -38,7 +38,7 @@ struct ProductParams {
     int32_t *err;
     uint64_t timeout_ns;
     int stall;
-    int split, stages;                           // few_kernel: CTAs of a cluster, stages of the ring
+    int nt, split, stages;                       // tokens of a tile, CTAs of a cluster, stages of the ring
 };
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A
@@ -59,6 +59,45 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b
                      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
                      ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
+
+// What bounds a CTA's waits: the first that runs out writes MOE_ETIMEOUT and
+// raises the flag, which ends the others.
+struct Bound {
+    uint64_t ns;
+    volatile int *abort;
+    int32_t *err;
+};
+
+// The phase of `bar` with `parity`, each lane for itself.  The clock is read
+// only once the wait has become long: reading it at every wait that did not
+// find its phase complete took longer than most of the waits.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Bound &b) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; i++) {
+        if (pipe::mbar_try_wait(bar, parity)) return true;
+        if (i % 32 == 0) {
+            if (*b.abort) return false;
+            const uint64_t t = pipe::globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > b.ns) {
+                atomicExch(b.err, MOE_ETIMEOUT);
+                *b.abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// A place in a ring of n, and the parity of the phase that its next turn is
+// waited for with.
+struct Ring {
+    int at = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++at == n) at = 0, turn ^= 1;
+    }
+};
 
 // NC accumulator columns of this warp's 32 lanes.
 template <int NC>
@@ -82,42 +121,46 @@ __device__ __forceinline__ void put(float *at, float v) { *at = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *at, float v) { *at = __float2bfloat16_rn(v); }
 
 // ---------------------------------------------------------------- few tokens
-// The weights are the 128 rows of the MMA and the tokens its NT columns, so
-// that a tile of weights is read once, for a token as for NT.  A cluster of
+// The weights are the 128 rows of the MMA and the tokens its `nt` columns, so
+// that a tile of weights is read once, for a token as for 256.  A cluster of
 // `split` CTAs shares a tile's blocks of K and joins the sums through
 // distributed shared memory, in the order of its CTAs.
-constexpr int kFewThreads = 192;         // warps 0-3 sums, 4 TMA, 5 MMA
 constexpr int kFewMaxStages = 12;
 constexpr int kFewScales = 64;           // blocks whose scales stand in shared memory at a time
-template <int NT>
+template <int MAXN>
 struct Few {
-    static constexpr int kSlots = NT <= 64 ? 4 : 2;                 // accumulators
-    static constexpr int kCols = kSlots * NT;                       // TMEM columns: 64 to 256
-    static constexpr int kStage = 128 * 128 + NT * 128;
+    static constexpr int kSumWarps = MAXN >= 64 ? 8 : 4;            // four a half of the columns, or of all
+    static constexpr int kCols = MAXN / (kSumWarps / 4);            // columns of a thread, at most
+    static constexpr int kSlots = MAXN <= 64 ? 4 : 2;               // accumulators
+    static constexpr int kTmem = kSlots * MAXN;                     // TMEM columns: 64 to 512
+    static constexpr int kThreads = 32 * (kSumWarps + 2);           // and a warp for TMA, one for the MMAs
 };
 
 // Blocks of a CTA, at most.
 __host__ __device__ inline int few_share(int KB, int split) { return (KB + split - 1) / split; }
 __host__ __device__ inline int few_scales(int KB, int split) { return min(few_share(KB, split), kFewScales); }
+__host__ __device__ inline int few_stage(int nt) { return 128 * 128 + nt * 128; }
 
-template <int NT>
-size_t few_smem(int KB, int split, int stages) {
-    return 1024 + (size_t)stages * Few<NT>::kStage + (size_t)few_scales(KB, split) * NT * 4 + (2 * kFewMaxStages + 2 * Few<NT>::kSlots + 1) * 8 + 16;
+template <int MAXN>
+size_t few_smem(int KB, int split, int stages, int nt) {
+    return 1024 + (size_t)stages * few_stage(nt) + (size_t)few_scales(KB, split) * MAXN * 4 + (2 * kFewMaxStages + 2 * Few<MAXN>::kSlots + 2) * 8 + 16;
 }
 
-template <int NT, typename O>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                                                          const ProductParams p) {
-    using F = Few<NT>;
+template <int MAXN, typename O>
+__global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                                                                  const ProductParams p) {
+    using F = Few<MAXN>;
     extern __shared__ __align__(1024) uint8_t smdyn[];
     uint8_t *stages = smdyn + ((1024u - (saddr(smdyn) & 1023u)) & 1023u);
-    float *scales = reinterpret_cast<float *>(stages + (size_t)p.stages * F::kStage);           // [blocks][NT]
-    uint64_t *full = reinterpret_cast<uint64_t *>(scales + few_scales(p.KB, p.split) * NT);
+    const int NT = p.nt, stage_bytes = few_stage(NT), S = p.split;
+    float *scales = reinterpret_cast<float *>(stages + (size_t)p.stages * stage_bytes);         // [blocks][MAXN]
+    uint64_t *full = reinterpret_cast<uint64_t *>(scales + few_scales(p.KB, S) * MAXN);
     uint64_t *empty = full + kFewMaxStages, *acc_full = empty + kFewMaxStages, *acc_empty = acc_full + F::kSlots;
-    uint64_t *stall_bar = acc_empty + F::kSlots;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(stall_bar + 1);
+    uint64_t *stall_bar = acc_empty + F::kSlots, *drain_bar = stall_bar + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = p.split;
+    const Bound bound{p.timeout_ns, abort_flag, p.err};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S, t0 = blockIdx.y * NT;
     const int kb0 = (int)((int64_t)p.KB * rank / S), nkb = (int)((int64_t)p.KB * (rank + 1) / S) - kb0;
     if (threadIdx.x == 0) {
@@ -127,14 +170,19 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         }
         for (int k = 0; k < F::kSlots; k++) {
             mbar_init(acc_full + k, 1);
-            mbar_init(acc_empty + k, 4);
+            mbar_init(acc_empty + k, F::kSumWarps);
         }
         mbar_init(stall_bar, 1);
+        mbar_init(drain_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)), "n"(F::kCols) : "memory");
+    if (warp == F::kSumWarps) {
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
+        if (lane == 1) asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+    }
+    if (warp == F::kSumWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)), "n"(F::kTmem) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
@@ -142,26 +190,27 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp == 4) {
+    if (warp == F::kSumWarps) {
         // the first fills all at once, a lane for each copy
         const int n0 = min(nkb, p.stages);
         if (lane < 2 * n0) {
             const int q = lane >> 1;
-            uint8_t *stage = stages + (size_t)q * F::kStage;
+            uint8_t *stage = stages + (size_t)q * stage_bytes;
             if (lane & 1) {
                 pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + q);
             } else {
-                mbar_expect_tx(full + q, F::kStage);
+                mbar_expect_tx(full + q, stage_bytes);
                 pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + q);
             }
         }
         __syncwarp();
         int q = n0;
-        for (; q < nkb; q++) {
-            const int s = q % p.stages;
-            uint8_t *stage = stages + (size_t)s * F::kStage;
-            if (!uwait(empty + s, ((q / p.stages) - 1) & 1, p.timeout_ns, abort_flag, p.err)) break;
-            if (lane == 0) mbar_expect_tx(full + s, F::kStage);
+        Ring r;
+        for (; q < nkb; q++, r.next(p.stages)) {
+            const int s = r.at;
+            uint8_t *stage = stages + (size_t)s * stage_bytes;
+            if (!__all_sync(0xffffffffu, wait(empty + s, r.turn, bound))) break;
+            if (lane == 0) mbar_expect_tx(full + s, stage_bytes);
             __syncwarp();
             if (lane == 0) pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + s);
             else if (lane == 1) pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + s);
@@ -172,132 +221,413 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             const int last = q - 1 - ((q - 1 - s) % p.stages);
             if (!pipe::warp_wait(full + s, (last / p.stages) & 1, p.timeout_ns) && lane == 0) atomicExch(p.err, MOE_ETIMEOUT);
         }
-    } else if (warp == 5) {
-        for (int q = 0; q < nkb; q++) {
-            const int s = q % p.stages, k = q % F::kSlots;
-            const bool have = uwait(full + s, (q / p.stages) & 1, p.timeout_ns, abort_flag, p.err);
-            const bool free = q < F::kSlots || uwait(acc_empty + k, ((q / F::kSlots) - 1) & 1, p.timeout_ns, abort_flag, p.err);
+    } else if (warp == F::kSumWarps + 1) {
+        const uint32_t idesc = idesc_e4m3(128, NT);
+        bool ok = true;
+        Ring r;
+        for (int q = 0; q < nkb && ok; q++, r.next(p.stages)) {
+            const int s = r.at, k = q % F::kSlots;
+            ok = wait(full + s, r.turn, bound) && (q < F::kSlots || wait(acc_empty + k, ((q / F::kSlots) - 1) & 1, bound));
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            if (lane == 0) {
-                if (have && free && !*abort_flag) {
-                    const uint64_t a = sw128_desc(saddr(stages + (size_t)s * F::kStage)), b = sw128_desc(saddr(stages + (size_t)s * F::kStage + 128 * 128));
+            if (lane == 0 && ok) {
+                const uint32_t at = saddr(stages + (size_t)s * stage_bytes);
+                const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
 #pragma unroll
-                    for (int kk = 0; kk < 4; kk++)                   // 32 bytes of K each
-                        mma_e4m3<1>(tmem + k * NT, a + 2 * kk, b + 2 * kk, idesc_e4m3(128, NT), kk > 0);
-                }
+                for (int kk = 0; kk < 4; kk++)                       // 32 bytes of K each
+                    mma_e4m3<1>(tmem + k * MAXN, a + 2 * kk, b + 2 * kk, idesc, kk > 0);
                 umma::umma_commit(empty + s);
                 umma::umma_commit(acc_full + k);
             }
             __syncwarp();
         }
+        if (!ok) {                           // what has been issued ends before the memory goes
+            if (lane == 0) umma::umma_commit(drain_bar);
+            __syncwarp();
+            pipe::warp_wait(drain_bar, 0, p.timeout_ns);
+        }
     } else {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, row = tid & 127;
         if (p.stall && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {        // test hook: bytes that no copy sends
             if (lane == 0) mbar_expect_tx(stall_bar, 16);
             __syncwarp();
-            uwait(stall_bar, 0, p.timeout_ns, abort_flag, p.err);
+            wait(stall_bar, 0, bound);
         }
-        float acc[NT];
+        // this warp's columns: from c0, nc of them (a multiple of 16)
+        const int half = F::kSumWarps == 8 ? (NT / 16 + 1) / 2 * 16 : NT;
+        const int c0 = F::kSumWarps == 8 && warp >= 4 ? half : 0, nc = min(half, NT - c0);
+        constexpr int NC = F::kCols < 32 ? 16 : 32;
+        float acc[F::kCols];
 #pragma unroll
-        for (int j = 0; j < NT; j++) acc[j] = 0.0f;
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        for (int j = 0; j < F::kCols; j++) acc[j] = 0.0f;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+        bool done = true;
         for (int q = 0; q < nkb; q++) {
             const int k = q % F::kSlots;
             if (q % kFewScales == 0) {
                 // the products of the next blocks' scales (the first while the tiles are on their way)
-                if (q) asm volatile("bar.sync 1, 128;" ::: "memory");
-                for (int i = tid; i < min(nkb - q, kFewScales) * NT; i += 128) {
-                    const int b = kb0 + q + i / NT, t = t0 + i % NT;
-                    scales[i] = t < p.T ? __ldg(p.sx + (size_t)t * p.sx_stride + b) * __ldg(p.sw + (size_t)tile * p.sw_stride + b) : 0.0f;
+                if (q) asm volatile("bar.sync 1, %0;" ::"n"(F::kSumWarps * 32) : "memory");
+                for (int i = tid; i < min(nkb - q, kFewScales) * MAXN; i += F::kSumWarps * 32) {
+                    const int b = kb0 + q + i / MAXN, j = i % MAXN;
+                    scales[i] = j < NT && t0 + j < p.T ? __ldg(p.sx + (size_t)(t0 + j) * p.sx_stride + b) * __ldg(p.sw + (size_t)tile * p.sw_stride + b) : 0.0f;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(F::kSumWarps * 32) : "memory");
             }
-            const bool ok = uwait(acc_full + k, (q / F::kSlots) & 1, p.timeout_ns, abort_flag, p.err);
+            done = __all_sync(0xffffffffu, wait(acc_full + k, (q / F::kSlots) & 1, bound));
+            if (!done) break;
             tc_fence_after();
-            // tcgen05.ld is warp-collective: the warp goes by lane 0's view
-            if (__shfl_sync(0xffffffffu, (int)(ok && !*abort_flag), 0)) {
-                constexpr int NC = NT < 32 ? 16 : 32;
-                const float4 *sc = reinterpret_cast<const float4 *>(scales + q % kFewScales * NT);
+            const float4 *sc = reinterpret_cast<const float4 *>(scales + q % kFewScales * MAXN + c0);
 #pragma unroll
-                for (int c = 0; c < NT; c += NC) {
-                    uint32_t d[NC];
-                    tmem_ld<NC>(lanes + k * NT + c, d);
+            for (int c = 0; c < F::kCols; c += NC) {
+                if (c >= nc) break;
+                uint32_t d[NC];
+                tmem_ld<NC>(lanes + k * MAXN + c, d);
 #pragma unroll
-                    for (int j = 0; j < NC; j += 4) {
-                        const float4 f = sc[(c + j) / 4];
-                        acc[c + j] = fmaf(f.x, __uint_as_float(d[j]), acc[c + j]);
-                        acc[c + j + 1] = fmaf(f.y, __uint_as_float(d[j + 1]), acc[c + j + 1]);
-                        acc[c + j + 2] = fmaf(f.z, __uint_as_float(d[j + 2]), acc[c + j + 2]);
-                        acc[c + j + 3] = fmaf(f.w, __uint_as_float(d[j + 3]), acc[c + j + 3]);
-                    }
+                for (int j = 0; j < NC; j += 4) {
+                    const float4 f = sc[(c + j) / 4];
+                    acc[c + j] = fmaf(f.x, __uint_as_float(d[j]), acc[c + j]);
+                    acc[c + j + 1] = fmaf(f.y, __uint_as_float(d[j + 1]), acc[c + j + 1]);
+                    acc[c + j + 2] = fmaf(f.z, __uint_as_float(d[j + 2]), acc[c + j + 2]);
+                    acc[c + j + 3] = fmaf(f.w, __uint_as_float(d[j + 3]), acc[c + j + 3]);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty + k);
         }
-        const int n = tile * 128 + tid, nt = min(NT, p.T - t0);
+        const int n = tile * 128 + row, have = min(nc, p.T - t0 - c0);
         if (S == 1) {
-            O *out = static_cast<O *>(p.out) + (size_t)t0 * p.out_stride + n;
+            O *out = static_cast<O *>(p.out) + (size_t)(t0 + c0) * p.out_stride + n;
             if (n < p.N) {
 #pragma unroll
-                for (int j = 0; j < NT; j++)
-                    if (j < nt) put(out + (size_t)j * p.out_stride, acc[j]);
+                for (int j = 0; j < F::kCols; j++)
+                    if (j < have) put(out + (size_t)j * p.out_stride, acc[j]);
             }
-        } else if (!*abort_flag) {
+        } else if (done) {
             // over the ring, all of whose copies and products are done: [token][row]
-            float *part = reinterpret_cast<float *>(stages);
+            float *part = reinterpret_cast<float *>(stages) + c0 * 128 + row;
 #pragma unroll
-            for (int j = 0; j < NT; j++)
-                if (j < nt) part[j * 128 + tid] = acc[j];
+            for (int j = 0; j < F::kCols; j++)
+                if (j < have) part[j * 128] = acc[j];
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == F::kSumWarps + 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::kTmem) : "memory");
     }
     if (S > 1) {
         cluster_sync();
-        const int n = tile * 128 + (int)threadIdx.x, nt = min(NT, p.T - t0);
-        if (threadIdx.x < 128 && n < p.N) {
-            const uint32_t mine = saddr(stages) + threadIdx.x * 4;
-            for (int j = rank; j < nt; j += S) {
-                float sum = 0.0f;
-                for (int r = 0; r < S; r++) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapped(mine + j * 512, r)) : "memory");
-                    sum += v;
-                }
-                put(static_cast<O *>(p.out) + (size_t)(t0 + j) * p.out_stride + n, sum);
-            }
+        // four rows of a token a thread, in turn among the cluster's threads
+        const uint32_t base = saddr(stages);
+        const int items = min(NT, p.T - t0) * 32;
+        for (int i = rank * F::kThreads + threadIdx.x; i < items; i += S * F::kThreads) {
+            const int j = i >> 5, n = tile * 128 + (i & 31) * 4;
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+                if (r < S)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w) : "r"(mapped(base + i * 16, r)));
+            float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int r = 1; r < 8; r++)
+                if (r < S) sum[0] += v[r].x, sum[1] += v[r].y, sum[2] += v[r].z, sum[3] += v[r].w;
+            O *out = static_cast<O *>(p.out) + (size_t)(t0 + j) * p.out_stride + n;
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                if (n + u < p.N) put(out + u, sum[u]);
         }
         cluster_sync();                  // no CTA's memory goes while another reads it
     }
 }
 
+// ---------------------------------------------------------------- many tokens
+// A pair of CTAs computes 256 tokens x 256 outputs: the tokens are the rows of
+// cta_group::2 MMAs (128 in each CTA's TMEM), so that a token's scale belongs
+// to a thread and a weight's to a whole warp, and each CTA brings the tiles of
+// its 128 tokens and of 128 of the outputs (a CTA of its own would have to
+// bring both halves: 48 KB a block of K instead of 32).  Two accumulators of 256 columns
+// fill TMEM; eight warps keep 128 sums a thread.  Persistent over the tiles,
+// eight rows of tiles at a time, so that the tiles in work share what L2 holds.
+constexpr int kManyStages = 5;
+constexpr int kManyStage = 2 * 128 * 128;
+constexpr int kManyThreads = 384;        // warps 0-7 sums, 8 TMA, 9 MMA (of the pair's first CTA); 10 and 11 fill the warpgroup
+// Registers: 168 a thread at launch; 256 threads with 128 sums take 208, the
+// other 128 keep 72: 256 * 208 + 128 * 72 <= 384 * 168.
+constexpr int kManySumRegs = 208, kManyOtherRegs = 72;
+static_assert(256 * kManySumRegs + 128 * kManyOtherRegs <= 384 * 168 && kManyThreads == 384, "within the launch's registers");
+constexpr int kManyBoxes = 8192;         // staging of a warp's results
+constexpr size_t kManySmem = 1024 + kManyStages * kManyStage + 8 * kManyBoxes + (2 * kManyStages + 6) * 8 + 16;
+constexpr int kManyRows = 8;             // rows of tiles that go together
+
+struct ManyParams {
+    const float *sx, *sw;
+    size_t sx_stride, sw_stride, out_stride;
+    int T, N, KB, tiles_m, tiles_n;
+    void *out;
+    int32_t *err;
+    uint64_t timeout_ns;
+    int stall;
+};
+
+__device__ __forceinline__ void many_tile(const ManyParams &p, int i, int &m, int &n) {
+    const int group = i / (kManyRows * p.tiles_n), rows = min(kManyRows, p.tiles_m - group * kManyRows), in = i - group * kManyRows * p.tiles_n;
+    n = in / rows;
+    m = group * kManyRows + in - n * rows;
+}
+
+// A copy of the pair: into this CTA's memory, told to the first CTA's barrier.
+__device__ __forceinline__ void tma_pair(void *dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(saddr(dst)), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(saddr(bar)), "h"((uint16_t)3) : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap *m, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(saddr(src)) : "memory");
+}
+
+// (d.lo, d.hi) * s + (a.lo, a.hi)
+__device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint64_t s) {
+    asm("{\n.reg .b64 d;\nmov.b64 d, {%1, %2};\nfma.rn.f32x2 %0, d, %3, %0;\n}\n" : "+l"(a) : "r"(lo), "r"(hi), "l"(s));
+}
+
+template <typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
+many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap, const ManyParams p) {
+    extern __shared__ __align__(1024) uint8_t smdyn[];
+    uint8_t *stages = smdyn + ((1024u - (saddr(smdyn) & 1023u)) & 1023u);
+    uint8_t *boxes = stages + kManyStages * kManyStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(boxes + 8 * kManyBoxes);
+    uint64_t *empty = full + kManyStages, *acc_full = empty + kManyStages, *acc_empty = acc_full + 2, *stall_bar = acc_empty + 2, *drain_bar = stall_bar + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    const Bound bound{p.timeout_ns, abort_flag, p.err};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
+    const int tiles = p.tiles_m * p.tiles_n, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int mine = tiles > pair ? (tiles - 1 - pair) / pairs + 1 : 0, nq = mine * p.KB;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kManyStages; s++) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int k = 0; k < 2; k++) {
+            mbar_init(acc_full + k, 1);
+            mbar_init(acc_empty + k, 16);
+        }
+        mbar_init(stall_bar, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_holder)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyOtherRegs));
+    if (warp == 8) {
+        int q = 0, kb = 0, li = 0, m = 0, n = 0;
+        if (nq) many_tile(p, pair, m, n);
+        Ring r;
+        for (; q < nq; q++, r.next(kManyStages)) {
+            const int s = r.at;
+            uint8_t *stage = stages + s * kManyStage;
+            if (q >= kManyStages && !__all_sync(0xffffffffu, wait(empty + s, r.turn ^ 1, bound))) break;
+            const uint32_t bar = mapped(saddr(full + s), 0);
+            if (lane == 0 && rank == 0) mbar_expect_tx(full + s, 2 * kManyStage);
+            __syncwarp();
+            if (lane == 0) tma_pair(stage, &xmap, kb * 128, m * 256 + rank * 128, bar);
+            else if (lane == 1) tma_pair(stage + 128 * 128, &wmap, kb * 128, n * 256 + rank * 128, bar);
+            __syncwarp();
+            if (++kb == p.KB) {
+                kb = 0;
+                if (++li < mine) many_tile(p, pair + li * pairs, m, n);
+            }
+        }
+        // the last fill of each stage, the other CTA's part too, lands before the pair exits
+        for (int s = 0; rank == 0 && s < kManyStages && s < q; s++) {
+            const int last = q - 1 - ((q - 1 - s) % kManyStages);
+            if (!pipe::warp_wait(full + s, (last / kManyStages) & 1, p.timeout_ns) && lane == 0) atomicExch(p.err, MOE_ETIMEOUT);
+        }
+    } else if (warp == 9 && rank == 0) {
+        bool ok = true;
+        Ring r;
+        for (int q = 0; q < nq && ok; q++, r.next(kManyStages)) {
+            const int s = r.at, k = q & 1;
+            ok = wait(full + s, r.turn, bound) && (q < 2 || wait(acc_empty + k, ((q >> 1) - 1) & 1, bound));
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (lane == 0 && ok) {
+                const uint32_t at = saddr(stages + s * kManyStage);
+                const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
+#pragma unroll
+                for (int kk = 0; kk < 4; kk++)
+                    mma_e4m3<2>(tmem + k * 256, a + 2 * kk, b + 2 * kk, idesc_e4m3(256, 256), kk > 0);
+                commit_pair(empty + s);
+                commit_pair(acc_full + k);
+            }
+            __syncwarp();
+        }
+        if (!ok) {                           // what has been issued ends before the memory goes
+            if (lane == 0) commit_pair(drain_bar);
+            __syncwarp();
+            pipe::warp_wait(drain_bar, 0, p.timeout_ns);
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManySumRegs));
+        if (p.stall && blockIdx.x == 0 && warp == 0) {                     // test hook: bytes that no copy sends
+            if (lane == 0) mbar_expect_tx(stall_bar, 16);
+            __syncwarp();
+            wait(stall_bar, 0, bound);
+        }
+        const int h = warp >> 2;                                           // half of the columns
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 128;
+        uint8_t *box = boxes + warp * kManyBoxes;
+        const uint32_t free_bar = mapped(saddr(acc_empty), 0);
+        int q = 0;
+        bool done = true;
+        for (int li = 0; li < mine && done; li++) {
+            int m, n;
+            many_tile(p, pair + li * pairs, m, n);
+            const int t = m * 256 + rank * 128 + (warp & 3) * 32 + lane, n0 = n * 256 + h * 128;
+            // rows behind the end have scales of 0, columns those of the last block
+            const float *sx = p.sx + (size_t)min(t, p.T - 1) * p.sx_stride;
+            const float *sw = p.sw + (size_t)min(n0 >> 7, (p.N - 1) >> 7) * p.sw_stride;
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; j++) acc[j] = 0;
+            float next = __ldg(sx) * __ldg(sw);
+            for (int kb = 0; kb < p.KB && done; kb++, q++) {
+                const int k = q & 1;
+                const uint32_t s1 = __float_as_uint(next);
+                uint64_t s2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(s1));
+                if (kb + 1 < p.KB) next = __ldg(sx + kb + 1) * __ldg(sw + kb + 1);
+                done = __all_sync(0xffffffffu, wait(acc_full + k, (q >> 1) & 1, bound));
+                tc_fence_after();
+                if (done) {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t d[32];
+                        umma::tmem_ld_x32(lanes + k * 256 + c, d);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) fma2(acc[(c + j) / 2], d[j], d[j + 1], s2);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(free_bar + k * 8) : "memory");
+            }
+            if (!done) break;
+            // this warp's 32 x 128 results, in boxes of 128 bytes a row whose 16-byte
+            // pieces stand as TMA's 128-byte swizzle has them (no bank conflicts)
+            constexpr int PER = 128 / sizeof(O), ROUND = kManyBoxes / 4096;        // columns of a box; boxes at a time
+            const int whole = p.N & ~(16 / (int)sizeof(O) - 1);
+            const int t_warp = t - lane;
+#pragma unroll
+            for (int c = 0; c < 128; c += PER * ROUND) {
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int b = 0; b < ROUND; b++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        uint4 w;
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 16 / (int)sizeof(O); j++) {
+                            const int col = c + b * PER + i * (16 / (int)sizeof(O)) + j;
+                            f[j] = __uint_as_float((uint32_t)(acc[col / 2] >> (col & 1 ? 32 : 0)));
+                        }
+                        if constexpr (sizeof(O) == 2) w = bf16x8(f);
+                        else w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                        *reinterpret_cast<uint4 *>(box + b * 4096 + lane * 128 + ((i ^ (lane & 7)) << 4)) = w;
+                    }
+                umma::fence_async_shared();
+                __syncwarp();
+                if (lane == 0 && t_warp < p.T) {
+#pragma unroll
+                    for (int b = 0; b < ROUND; b++)
+                        if (n0 + c + b * PER < whole) tma_store(&omap, box + b * 4096, n0 + c + b * PER, t_warp);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+            // TMA writes whole 16-byte pieces: what is left of the rows goes by itself
+            if (whole < p.N && n0 < p.N && n0 + 128 > whole && t < p.T) {
+                O *out = static_cast<O *>(p.out) + (size_t)t * p.out_stride + n0;
+#pragma unroll
+                for (int c = 0; c < 128; c++)
+                    if (n0 + c >= whole && n0 + c < p.N) put(out + c, __uint_as_float((uint32_t)(acc[c / 2] >> (c & 1 ? 32 : 0))));
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                      // the other CTA's arrivals and products are done too
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host
 int encode_tile(CUtensorMap *m, const void *base, size_t rows, size_t cols, size_t stride, int box_rows) {
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {rows > 1 ? stride : align_up(cols, 16)};
     const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
     return pipe::encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NT, typename O>
-int launch_few(const CUtensorMap &wmap, const CUtensorMap &xmap, ProductParams p, cudaStream_t st) {
-    const int tiles = (p.N - 1) / 128 + 1, cols = (p.T - 1) / NT + 1;
-    p.split = 1;
-    while (p.split < 8 && 2 * p.split <= p.KB && (int64_t)tiles * cols * p.split * 2 <= 2 * num_sms()) p.split *= 2;
-    p.stages = std::min(std::max(2, few_share(p.KB, p.split)), std::min(kFewMaxStages, (100 << 10) / Few<NT>::kStage));
-    p.stages = std::max(p.stages, (NT * 512 + Few<NT>::kStage - 1) / Few<NT>::kStage);       // room for the sums
-    const size_t smem = few_smem<NT>(p.KB, p.split, p.stages);
+int no_map() { return fail(MOE_ECUDA, "scaled_product: no tensor map"); }
+
+template <typename O>
+int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, const ProductParams &q, cudaStream_t st) {
+    CUtensorMap xmap, wmap, omap;
+    const cuuint64_t dims[2] = {std::max<cuuint64_t>(16 / sizeof(O), q.N / (16 / sizeof(O)) * (16 / sizeof(O))), (cuuint64_t)q.T}, strides[1] = {(q.T > 1 ? q.out_stride : align_up(q.N, 8)) * sizeof(O)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(O)), 32};
+    if (encode_tile(&xmap, x, q.T, wd->K, x_stride, 128) || encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 128) ||
+        pipe::encode_map(&omap, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q.out, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+        return no_map();
     static OnDevices ready;
-    cudaError_t e = ready.once([] { return cudaFuncSetAttribute(few_kernel<NT, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10); });
+    const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kManySmem); });
+    if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
+    const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / 256 + 1, q.out, q.err, q.timeout_ns, q.stall};
+    const int pairs = (int)std::min<int64_t>(num_sms() / 2, (int64_t)p.tiles_m * p.tiles_n);
+    many_kernel<O><<<2 * pairs, kManyThreads, kManySmem, st>>>(xmap, wmap, omap, p);
+    return check_launch("many_kernel");
+}
+
+template <int MAXN, typename O>
+int launch_few(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, ProductParams p, cudaStream_t st) {
+    CUtensorMap wmap, xmap;
+    if (encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 128) || encode_tile(&xmap, x, p.T, wd->K, x_stride, p.nt)) return no_map();
+    const int tiles = (p.N - 1) / 128 + 1, cols = (p.T - 1) / p.nt + 1;
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split <= p.KB && (int64_t)tiles * cols * p.split * 2 <= (p.nt <= 128 ? 2 : 1) * num_sms()) p.split *= 2;
+    const int stage = few_stage(p.nt), least = std::max(2, p.split > 1 ? (p.nt * 512 + stage - 1) / stage : 2);      // room for the sums
+    p.stages = std::max(least, std::min({few_share(p.KB, p.split), kFewMaxStages, (MAXN <= 128 ? 100 << 10 : 160 << 10) / stage}));
+    static OnDevices ready;
+    cudaError_t e = ready.once([] { return cudaFuncSetAttribute(few_kernel<MAXN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10); });
     if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split), (unsigned)cols);
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(Few<MAXN>::kThreads);
+    cfg.dynamicSmemBytes = few_smem<MAXN>(p.KB, p.split, p.stages, p.nt);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -305,23 +635,24 @@ int launch_few(const CUtensorMap &wmap, const CUtensorMap &xmap, ProductParams p
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, few_kernel<NT, O>, wmap, xmap, p);
+    e = cudaLaunchKernelEx(&cfg, few_kernel<MAXN, O>, wmap, xmap, p);
     if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
     return check_launch("few_kernel");
 }
 
 template <typename O>
-int launch_product(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, const ProductParams &p, cudaStream_t st) {
-    CUtensorMap wmap, xmap;
-    const int nt = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
-    if (encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 128) || encode_tile(&xmap, x, p.T, wd->K, x_stride, nt))
-        return fail(MOE_ECUDA, "scaled_product: no tensor map");
-    switch (nt) {
-    case 16: return launch_few<16, O>(wmap, xmap, p, st);
-    case 32: return launch_few<32, O>(wmap, xmap, p, st);
-    case 64: return launch_few<64, O>(wmap, xmap, p, st);
-    default: return launch_few<128, O>(wmap, xmap, p, st);
-    }
+int launch_product(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, ProductParams p, cudaStream_t st) {
+    // Tokens in one row of tiles, or as many rows as the SMs take at a time.
+    const int64_t tiles = (p.N - 1) / 128 + 1;
+    const char *force = getenv("MANY");
+    if (force ? atoi(force) : p.T > 1024) return launch_many<O>(x, x_stride, wd, p, st);
+    int64_t rows = std::max<int64_t>((p.T - 1) / 256 + 1, std::min<int64_t>(num_sms() / tiles, (p.T - 1) / 128 + 1));
+    p.nt = (int)(((p.T - 1) / rows + 1 + 15) / 16 * 16);
+    if (p.nt <= 16) return launch_few<16, O>(x, x_stride, wd, p, st);
+    if (p.nt <= 32) return launch_few<32, O>(x, x_stride, wd, p, st);
+    if (p.nt <= 64) return launch_few<64, O>(x, x_stride, wd, p, st);
+    if (p.nt <= 128) return launch_few<128, O>(x, x_stride, wd, p, st);
+    return launch_few<256, O>(x, x_stride, wd, p, st);
 }
 
 int check_matrix(const moe_scaled_matrix_desc *wd, const char *who) {
