@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         // this warp's columns: from c0, nc of them (a multiple of 16)
         const int half = F::kSumWarps == 8 ? (NT / 16 + 1) / 2 * 16 : NT;
         const int c0 = F::kSumWarps == 8 && warp >= 4 ? half : 0, nc = min(half, NT - c0);
-        constexpr int NC = F::kCols < 32 ? 16 : 32;
+        constexpr int NC = F::kCols < 32 || F::kCols > 64 ? 16 : 32;          // (32 beside 128 sums do not fit the registers)
         float acc[F::kCols];
 #pragma unroll
         for (int j = 0; j < F::kCols; j++) acc[j] = 0.0f;
@@ -267,9 +267,19 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
             if (q % kFewScales == 0) {
                 // the products of the next blocks' scales (the first while the tiles are on their way)
                 if (q) asm volatile("bar.sync 1, %0;" ::"n"(F::kSumWarps * 32) : "memory");
-                for (int i = tid; i < min(nkb - q, kFewScales) * MAXN; i += F::kSumWarps * 32) {
-                    const int b = kb0 + q + i / MAXN, j = i % MAXN;
-                    scales[i] = j < NT && t0 + j < p.T ? __ldg(p.sx + (size_t)(t0 + j) * p.sx_stride + b) * __ldg(p.sw + (size_t)tile * p.sw_stride + b) : 0.0f;
+                const int all = min(nkb - q, kFewScales) * MAXN;
+                for (int i0 = tid; i0 < all; i0 += 8 * F::kSumWarps * 32) {
+                    float x[8], w[8];
+#pragma unroll
+                    for (int u = 0; u < 8; u++) {
+                        const int i = i0 + u * F::kSumWarps * 32, b = kb0 + q + i / MAXN, j = i % MAXN;
+                        const bool in = i < all && j < NT && t0 + j < p.T;
+                        x[u] = in ? __ldg(p.sx + (size_t)(t0 + j) * p.sx_stride + b) : 0.0f;
+                        w[u] = in ? __ldg(p.sw + (size_t)tile * p.sw_stride + b) : 0.0f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        if (i0 + u * F::kSumWarps * 32 < all) scales[i0 + u * F::kSumWarps * 32] = x[u] * w[u];
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(F::kSumWarps * 32) : "memory");
             }
@@ -509,22 +519,22 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; j++) acc[j] = 0;
-            float next = __ldg(sx) * __ldg(sw);
+            float next_x = __ldg(sx), next_w = __ldg(sw);              // (their product waits for the loads: a block later)
             for (int kb = 0; kb < p.KB && done; kb++, q++) {
                 const int k = q & 1;
-                const uint32_t s1 = __float_as_uint(next);
+                const uint32_t s1 = __float_as_uint(next_x * next_w);
                 uint64_t s2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(s1));
-                if (kb + 1 < p.KB) next = __ldg(sx + kb + 1) * __ldg(sw + kb + 1);
+                if (kb + 1 < p.KB) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
                 done = __all_sync(0xffffffffu, wait(acc_full + k, (q >> 1) & 1, bound));
                 tc_fence_after();
                 if (done) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        uint32_t d[32];
-                        umma::tmem_ld_x32(lanes + k * 256 + c, d);
+                    for (int c = 0; c < 128; c += 16) {
+                        uint32_t d[16];
+                        umma::tmem_ld_x16(lanes + k * 256 + c, d);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) fma2(acc[(c + j) / 2], d[j], d[j + 1], s2);
+                        for (int j = 0; j < 16; j += 2) fma2(acc[(c + j) / 2], d[j], d[j + 1], s2);
                     }
                 }
                 tc_fence_before();
