@@ -89,6 +89,16 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Bound
     }
 }
 
+// One lane of a warp that runs together.  The tensor cores' and TMA's
+// instructions take uniform registers, and the compiler keeps what such a lane
+// computes there: four MMAs, their two commits and a wait take 190 clocks to
+// issue, and 335 behind a test of the lane's number.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
 // A place in a ring of n, and the parity of the phase that its next turn is
 // waited for with.
 struct Ring {
@@ -205,17 +215,17 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         }
         __syncwarp();
         int q = n0;
-        Ring r;
-        for (; q < nkb; q++, r.next(p.stages)) {
-            const int s = r.at;
-            uint8_t *stage = stages + (size_t)s * stage_bytes;
-            if (!__all_sync(0xffffffffu, wait(empty + s, r.turn, bound))) break;
-            if (lane == 0) mbar_expect_tx(full + s, stage_bytes);
-            __syncwarp();
-            if (lane == 0) pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + s);
-            else if (lane == 1) pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + s);
-            __syncwarp();
+        if (elected()) {
+            Ring r;
+            for (; q < nkb; q++, r.next(p.stages)) {
+                uint8_t *stage = stages + (size_t)r.at * stage_bytes;
+                if (!wait(empty + r.at, r.turn, bound)) break;
+                mbar_expect_tx(full + r.at, stage_bytes);
+                pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + r.at);
+                pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + r.at);
+            }
         }
+        q = __reduce_max_sync(0xffffffffu, (unsigned)q);
         // the last fill of each stage lands before the CTA exits
         for (int s = 0; s < p.stages && s < q; s++) {
             const int last = q - 1 - ((q - 1 - s) % p.stages);
@@ -224,23 +234,23 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
     } else if (warp == F::kSumWarps + 1) {
         const uint32_t idesc = idesc_e4m3(128, NT);
         bool ok = true;
-        Ring r;
-        for (int q = 0; q < nkb && ok; q++, r.next(p.stages)) {
-            const int s = r.at, k = q % F::kSlots;
-            ok = wait(full + s, r.turn, bound) && (q < F::kSlots || wait(acc_empty + k, ((q / F::kSlots) - 1) & 1, bound));
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            if (lane == 0 && ok) {
-                const uint32_t at = saddr(stages + (size_t)s * stage_bytes);
+        if (elected()) {
+            Ring r;
+            for (int q = 0; q < nkb && ok; q++, r.next(p.stages)) {
+                const int k = q % F::kSlots;
+                ok = wait(full + r.at, r.turn, bound) && (q < F::kSlots || wait(acc_empty + k, ((q / F::kSlots) - 1) & 1, bound));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = saddr(stages + (size_t)r.at * stage_bytes);
                 const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
 #pragma unroll
                 for (int kk = 0; kk < 4; kk++)                       // 32 bytes of K each
                     mma_e4m3<1>(tmem + k * MAXN, a + 2 * kk, b + 2 * kk, idesc, kk > 0);
-                umma::umma_commit(empty + s);
                 umma::umma_commit(acc_full + k);
+                if (q + p.stages < nkb) umma::umma_commit(empty + r.at);         // (nothing waits for the last ones)
             }
-            __syncwarp();
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {                           // what has been issued ends before the memory goes
             if (lane == 0) umma::umma_commit(drain_bar);
             __syncwarp();
@@ -358,7 +368,8 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
 // to a thread and a weight's to a whole warp, and each CTA brings the tiles of
 // its 128 tokens and of 128 of the outputs (a CTA of its own would have to
 // bring both halves: 48 KB a block of K instead of 32).  Two accumulators of 256 columns
-// fill TMEM; eight warps keep 128 sums a thread.  Persistent over the tiles,
+// fill TMEM, each in two halves that are multiplied, read and freed by themselves (an accumulator's turn,
+// from one block's products to the next one's, is the shorter); eight warps keep 128 sums a thread.  Persistent over the tiles,
 // eight rows of tiles at a time, so that the tiles in work share what L2 holds.
 constexpr int kManyStages = 5;
 constexpr int kManyStage = 2 * 128 * 128;
@@ -368,7 +379,7 @@ constexpr int kManyThreads = 384;        // warps 0-7 sums, 8 TMA, 9 MMA (of the
 constexpr int kManySumRegs = 208, kManyOtherRegs = 72;
 static_assert(256 * kManySumRegs + 128 * kManyOtherRegs <= 384 * 168 && kManyThreads == 384, "within the launch's registers");
 constexpr int kManyBoxes = 8192;         // staging of a warp's results
-constexpr size_t kManySmem = 1024 + kManyStages * kManyStage + 8 * kManyBoxes + (2 * kManyStages + 6) * 8 + 16;
+constexpr size_t kManySmem = 1024 + kManyStages * kManyStage + 8 * kManyBoxes + (2 * kManyStages + 10) * 8 + 16;
 constexpr int kManyRows = 8;             // rows of tiles that go together
 
 struct ManyParams {
@@ -414,7 +425,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     uint8_t *stages = smdyn + ((1024u - (saddr(smdyn) & 1023u)) & 1023u);
     uint8_t *boxes = stages + kManyStages * kManyStage;
     uint64_t *full = reinterpret_cast<uint64_t *>(boxes + 8 * kManyBoxes);
-    uint64_t *empty = full + kManyStages, *acc_full = empty + kManyStages, *acc_empty = acc_full + 2, *stall_bar = acc_empty + 2, *drain_bar = stall_bar + 1;
+    uint64_t *empty = full + kManyStages, *acc_full = empty + kManyStages, *acc_empty = acc_full + 4, *stall_bar = acc_empty + 4, *drain_bar = stall_bar + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     const Bound bound{p.timeout_ns, abort_flag, p.err};
@@ -426,9 +437,9 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
-        for (int k = 0; k < 2; k++) {
+        for (int k = 0; k < 4; k++) {
             mbar_init(acc_full + k, 1);
-            mbar_init(acc_empty + k, 16);
+            mbar_init(acc_empty + k, 8);
         }
         mbar_init(stall_bar, 1);
         mbar_init(drain_bar, 1);
@@ -450,22 +461,24 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     if (warp == 8) {
         int q = 0, kb = 0, li = 0, m = 0, n = 0;
         if (nq) many_tile(p, pair, m, n);
-        Ring r;
-        for (; q < nq; q++, r.next(kManyStages)) {
-            const int s = r.at;
-            uint8_t *stage = stages + s * kManyStage;
-            if (q >= kManyStages && !__all_sync(0xffffffffu, wait(empty + s, r.turn ^ 1, bound))) break;
-            const uint32_t bar = mapped(saddr(full + s), 0);
-            if (lane == 0 && rank == 0) mbar_expect_tx(full + s, 2 * kManyStage);
-            __syncwarp();
-            if (lane == 0) tma_pair(stage, &xmap, kb * 128, m * 256 + rank * 128, bar);
-            else if (lane == 1) tma_pair(stage + 128 * 128, &wmap, kb * 128, n * 256 + rank * 128, bar);
-            __syncwarp();
-            if (++kb == p.KB) {
-                kb = 0;
-                if (++li < mine) many_tile(p, pair + li * pairs, m, n);
+        if (elected()) {
+            const uint32_t first_full = mapped(saddr(full), 0);
+            Ring r;
+            for (; q < nq; q++, r.next(kManyStages)) {
+                uint8_t *stage = stages + r.at * kManyStage;
+                if (q >= kManyStages && !wait(empty + r.at, r.turn ^ 1, bound)) break;
+                const uint32_t bar = first_full + r.at * 8;
+                if (rank == 0) mbar_expect_tx(full + r.at, 2 * kManyStage);
+                tma_pair(stage, &xmap, kb * 128, m * 256 + rank * 128, bar);
+                tma_pair(stage + 128 * 128, &wmap, kb * 128, n * 256 + rank * 64, bar);
+                tma_pair(stage + 192 * 128, &wmap, kb * 128, n * 256 + 128 + rank * 64, bar);
+                if (++kb == p.KB) {
+                    kb = 0;
+                    if (++li < mine) many_tile(p, pair + li * pairs, m, n);
+                }
             }
         }
+        q = __reduce_max_sync(0xffffffffu, (unsigned)q);
         // the last fill of each stage, the other CTA's part too, lands before the pair exits
         for (int s = 0; rank == 0 && s < kManyStages && s < q; s++) {
             const int last = q - 1 - ((q - 1 - s) % kManyStages);
@@ -473,23 +486,27 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         }
     } else if (warp == 9 && rank == 0) {
         bool ok = true;
-        Ring r;
-        for (int q = 0; q < nq && ok; q++, r.next(kManyStages)) {
-            const int s = r.at, k = q & 1;
-            ok = wait(full + s, r.turn, bound) && (q < 2 || wait(acc_empty + k, ((q >> 1) - 1) & 1, bound));
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            if (lane == 0 && ok) {
+        if (elected()) {
+            Ring r;
+            for (int q = 0; q < nq && ok; q++, r.next(kManyStages)) {
+                const int s = r.at, k = 2 * (q & 1);
+                ok = wait(full + s, r.turn, bound);
                 const uint32_t at = saddr(stages + s * kManyStage);
                 const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
 #pragma unroll
-                for (int kk = 0; kk < 4; kk++)
-                    mma_e4m3<2>(tmem + k * 256, a + 2 * kk, b + 2 * kk, idesc_e4m3(256, 256), kk > 0);
-                commit_pair(empty + s);
-                commit_pair(acc_full + k);
+                for (int h = 0; h < 2; h++) {
+                    if (q >= 2) ok = ok && wait(acc_empty + k + h, ((q >> 1) - 1) & 1, bound);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; kk++)
+                        mma_e4m3<2>(tmem + (k + h) * 128, a + 2 * kk, b + (h * 64 * 128 >> 4) + 2 * kk, idesc_e4m3(256, 128), kk > 0);
+                    commit_pair(acc_full + k + h);
+                }
+                if (ok) commit_pair(empty + s);
             }
-            __syncwarp();
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {                           // what has been issued ends before the memory goes
             if (lane == 0) commit_pair(drain_bar);
             __syncwarp();
@@ -504,7 +521,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             wait(stall_bar, 0, bound);
         }
         const int h = warp >> 2;                                           // half of the columns
-        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 128;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         uint8_t *box = boxes + warp * kManyBoxes;
         const uint32_t free_bar = mapped(saddr(acc_empty), 0);
         int q = 0;
@@ -521,7 +538,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             for (int j = 0; j < 64; j++) acc[j] = 0;
             float next_x = __ldg(sx), next_w = __ldg(sw);              // (their product waits for the loads: a block later)
             for (int kb = 0; kb < p.KB && done; kb++, q++) {
-                const int k = q & 1;
+                const int k = 2 * (q & 1) + h;
                 const uint32_t s1 = __float_as_uint(next_x * next_w);
                 uint64_t s2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(s1));
@@ -532,7 +549,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                     for (int c = 0; c < 128; c += 16) {
                         uint32_t d[16];
-                        umma::tmem_ld_x16(lanes + k * 256 + c, d);
+                        umma::tmem_ld_x16(lanes + k * 128 + c, d);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) fma2(acc[(c + j) / 2], d[j], d[j + 1], s2);
                     }
@@ -609,7 +626,7 @@ int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd
     CUtensorMap xmap, wmap, omap;
     const cuuint64_t dims[2] = {std::max<cuuint64_t>(16 / sizeof(O), q.N / (16 / sizeof(O)) * (16 / sizeof(O))), (cuuint64_t)q.T}, strides[1] = {(q.T > 1 ? q.out_stride : align_up(q.N, 8)) * sizeof(O)};
     const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(O)), 32};
-    if (encode_tile(&xmap, x, q.T, wd->K, x_stride, 128) || encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 128) ||
+    if (encode_tile(&xmap, x, q.T, wd->K, x_stride, 128) || encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 64) ||
         pipe::encode_map(&omap, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q.out, dims, strides, box,
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return no_map();
