@@ -116,6 +116,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[NC]) {
     else umma::tmem_ld_x32(at, r);
 }
 
+// The same without the wait, and the wait: what is loaded stands in r behind it.
+__device__ __forceinline__ void tmem_ask(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(at));
+}
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
+}
+
 // Every thread of the cluster, once each.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
@@ -413,11 +422,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *m, const void *src,
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(saddr(src)) : "memory");
 }
 
-// (d.lo, d.hi) * s + (a.lo, a.hi)
-__device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint64_t s) {
-    asm("{\n.reg .b64 d;\nmov.b64 d, {%1, %2};\nfma.rn.f32x2 %0, d, %3, %0;\n}\n" : "+l"(a) : "r"(lo), "r"(hi), "l"(s));
-}
-
 template <typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
 many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap, const ManyParams p) {
@@ -533,25 +537,25 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             // rows behind the end have scales of 0, columns those of the last block
             const float *sx = p.sx + (size_t)min(t, p.T - 1) * p.sx_stride;
             const float *sw = p.sw + (size_t)min(n0 >> 7, (p.N - 1) >> 7) * p.sw_stride;
-            uint64_t acc[64];
+            float acc[128];
 #pragma unroll
-            for (int j = 0; j < 64; j++) acc[j] = 0;
+            for (int j = 0; j < 128; j++) acc[j] = 0.0f;
             float next_x = __ldg(sx), next_w = __ldg(sw);              // (their product waits for the loads: a block later)
             for (int kb = 0; kb < p.KB && done; kb++, q++) {
                 const int k = 2 * (q & 1) + h;
-                const uint32_t s1 = __float_as_uint(next_x * next_w);
-                uint64_t s2;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(s1));
+                const float scale = next_x * next_w;
                 if (kb + 1 < p.KB) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
                 done = __all_sync(0xffffffffu, wait(acc_full + k, (q >> 1) & 1, bound));
                 tc_fence_after();
                 if (done) {
+                    uint32_t d[2][16];
+                    tmem_ask(lanes + k * 128, d[0]);
 #pragma unroll
-                    for (int c = 0; c < 128; c += 16) {
-                        uint32_t d[16];
-                        umma::tmem_ld_x16(lanes + k * 128 + c, d);
+                    for (int c = 0; c < 8; c++) {
+                        tmem_got(d[c & 1]);
+                        if (c < 7) tmem_ask(lanes + k * 128 + (c + 1) * 16, d[(c + 1) & 1]);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) fma2(acc[(c + j) / 2], d[j], d[j + 1], s2);
+                        for (int j = 0; j < 16; j++) acc[16 * c + j] = fmaf(scale, __uint_as_float(d[c & 1][j]), acc[16 * c + j]);
                     }
                 }
                 tc_fence_before();
@@ -577,7 +581,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                         for (int j = 0; j < 16 / (int)sizeof(O); j++) {
                             const int col = c + b * PER + i * (16 / (int)sizeof(O)) + j;
-                            f[j] = __uint_as_float((uint32_t)(acc[col / 2] >> (col & 1 ? 32 : 0)));
+                            f[j] = acc[col];
                         }
                         if constexpr (sizeof(O) == 2) w = bf16x8(f);
                         else w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
@@ -597,7 +601,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 O *out = static_cast<O *>(p.out) + (size_t)t * p.out_stride + n0;
 #pragma unroll
                 for (int c = 0; c < 128; c++)
-                    if (n0 + c >= whole && n0 + c < p.N) put(out + c, __uint_as_float((uint32_t)(acc[c / 2] >> (c & 1 ? 32 : 0))));
+                    if (n0 + c >= whole && n0 + c < p.N) put(out + c, acc[c]);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
