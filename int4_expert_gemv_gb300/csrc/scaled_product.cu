@@ -36,7 +36,7 @@ struct ProductParams {
     int T, N, KB;
     void *out;
     int32_t *err;
-    uint64_t timeout_ns;
+    uint32_t polls;                              // of a wait, at most
     int stall;
     int nt, split, stages;                       // tokens of a tile, CTAs of a cluster, stages of the ring
 };
@@ -60,43 +60,42 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b
                      ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// What bounds a CTA's waits: the first that runs out writes MOE_ETIMEOUT and
-// raises the flag, which ends the others.
+// Waits for the phase of `bar` with `parity`.  Both kinds count polls, and
+// where those run out they write MOE_ETIMEOUT.
+//
+// The threads that issue copies and MMAs sleep between polls: a spinning one
+// takes issue slots from the sums' warps (8190 x 5120 x 4096: 136 us with the
+// sleep, 143 without; 157 with the hardware's own suspended wait, which wakes late).
 struct Bound {
-    uint64_t ns;
-    volatile int *abort;
+    uint32_t polls;
     int32_t *err;
 };
-
-// The phase of `bar` with `parity`, each lane for itself.  The clock is read
-// only once the wait has become long: reading it at every wait that did not
-// find its phase complete took longer than most of the waits.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Bound &b) {
-    uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t i = 1;; i++) {
+    for (uint32_t i = b.polls; i; i--) {
         if (pipe::mbar_try_wait(bar, parity)) return true;
-        if (i % 32 == 0) {
-            if (*b.abort) return false;
-            const uint64_t t = pipe::globaltimer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > b.ns) {
-                atomicExch(b.err, MOE_ETIMEOUT);
-                *b.abort = 1;
-                return false;
-            }
-        }
+        __nanosleep(32);
+    }
+    atomicExch(b.err, MOE_ETIMEOUT);
+    return false;
+}
+
+// Those that multiply and add go on with what there is when their polls, counted over the
+// whole kernel, have run out (the results are invalid then): with a way out of the
+// loop over the blocks the MMAs' issue is no longer uniform code to the compiler, and
+// 8190 x 5120 x 4096 takes 181 us instead of 136.
+template <bool SLEEP>
+__device__ __forceinline__ void wait_on(uint64_t *bar, uint32_t parity, int &left) {
+#pragma unroll 1
+    while (!pipe::mbar_try_wait(bar, parity)) {
+        if (--left <= 0) break;
+        if (SLEEP) __nanosleep(32);
     }
 }
 
-// One lane of a warp that runs together.  The tensor cores' and TMA's
-// instructions take uniform registers, and the compiler keeps what such a lane
-// computes there: four MMAs, their two commits and a wait take 190 clocks to
-// issue, and 335 behind a test of the lane's number.
-__device__ __forceinline__ bool elected() {
-    uint32_t one;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
-    return one != 0;
+// Polls of a whole kernel of n blocks: a wait's, and what waits take that are in time.
+__device__ __forceinline__ int all_polls(uint32_t polls, int n) {
+    return (int)min((uint64_t)polls * 2 + (uint64_t)n * 1024, (uint64_t)INT32_MAX);
 }
 
 // A place in a ring of n, and the parity of the phase that its next turn is
@@ -109,20 +108,21 @@ struct Ring {
     }
 };
 
+// One lane of a warp that runs together.  The tensor cores' and TMA's
+// instructions take uniform registers, and the compiler keeps what such a lane
+// computes there: four MMAs, their two commits and a wait take 190 clocks to
+// issue, and 335 behind a test of the lane's number.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
 // NC accumulator columns of this warp's 32 lanes.
 template <int NC>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[NC]) {
     if constexpr (NC == 16) umma::tmem_ld_x16(at, r);
     else umma::tmem_ld_x32(at, r);
-}
-
-// The same without the wait, and the wait: what is loaded stands in r behind it.
-__device__ __forceinline__ void tmem_ask(uint32_t at, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(at));
-}
-__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
 }
 
 // Every thread of the cluster, once each.
@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
     uint64_t *empty = full + kFewMaxStages, *acc_full = empty + kFewMaxStages, *acc_empty = acc_full + F::kSlots;
     uint64_t *stall_bar = acc_empty + F::kSlots, *drain_bar = stall_bar + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    const Bound bound{p.timeout_ns, abort_flag, p.err};
+    const Bound bound{p.polls, p.err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S, t0 = blockIdx.y * NT;
     const int kb0 = (int)((int64_t)p.KB * rank / S), nkb = (int)((int64_t)p.KB * (rank + 1) / S) - kb0;
@@ -193,7 +192,6 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         }
         mbar_init(stall_bar, 1);
         mbar_init(drain_bar, 1);
-        *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == F::kSumWarps) {
@@ -238,17 +236,17 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         // the last fill of each stage lands before the CTA exits
         for (int s = 0; s < p.stages && s < q; s++) {
             const int last = q - 1 - ((q - 1 - s) % p.stages);
-            if (!pipe::warp_wait(full + s, (last / p.stages) & 1, p.timeout_ns) && lane == 0) atomicExch(p.err, MOE_ETIMEOUT);
+            wait(full + s, (last / p.stages) & 1, bound);
         }
     } else if (warp == F::kSumWarps + 1) {
         const uint32_t idesc = idesc_e4m3(128, NT);
-        bool ok = true;
         if (elected()) {
+            int left = all_polls(p.polls, nkb);
             Ring r;
-            for (int q = 0; q < nkb && ok; q++, r.next(p.stages)) {
+            for (int q = 0; q < nkb; q++, r.next(p.stages)) {
                 const int k = q % F::kSlots;
-                ok = wait(full + r.at, r.turn, bound) && (q < F::kSlots || wait(acc_empty + k, ((q / F::kSlots) - 1) & 1, bound));
-                if (!ok) break;
+                wait_on<true>(full + r.at, r.turn, left);
+                if (q >= F::kSlots) wait_on<true>(acc_empty + k, ((q / F::kSlots) - 1) & 1, left);
                 tc_fence_after();
                 const uint32_t at = saddr(stages + (size_t)r.at * stage_bytes);
                 const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
@@ -258,13 +256,11 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
                 umma::umma_commit(acc_full + k);
                 if (q + p.stages < nkb) umma::umma_commit(empty + r.at);         // (nothing waits for the last ones)
             }
+            umma::umma_commit(drain_bar);
+            if (left <= 0) atomicExch(p.err, MOE_ETIMEOUT);
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {                           // what has been issued ends before the memory goes
-            if (lane == 0) umma::umma_commit(drain_bar);
-            __syncwarp();
-            pipe::warp_wait(drain_bar, 0, p.timeout_ns);
-        }
+        __syncwarp();
+        wait(drain_bar, 0, bound);           // what has been issued ends before the memory goes
     } else {
         const int tid = threadIdx.x, row = tid & 127;
         if (p.stall && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {        // test hook: bytes that no copy sends
@@ -280,7 +276,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < F::kCols; j++) acc[j] = 0.0f;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
-        bool done = true;
+        int left = all_polls(p.polls, nkb);
         for (int q = 0; q < nkb; q++) {
             const int k = q % F::kSlots;
             if (q % kFewScales == 0) {
@@ -302,8 +298,8 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(F::kSumWarps * 32) : "memory");
             }
-            done = __all_sync(0xffffffffu, wait(acc_full + k, (q / F::kSlots) & 1, bound));
-            if (!done) break;
+            wait_on<false>(acc_full + k, (q / F::kSlots) & 1, left);
+            __syncwarp();
             tc_fence_after();
             const float4 *sc = reinterpret_cast<const float4 *>(scales + q % kFewScales * MAXN + c0);
 #pragma unroll
@@ -324,6 +320,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty + k);
         }
+        if (left <= 0) atomicExch(p.err, MOE_ETIMEOUT);
         const int n = tile * 128 + row, have = min(nc, p.T - t0 - c0);
         if (S == 1) {
             O *out = static_cast<O *>(p.out) + (size_t)(t0 + c0) * p.out_stride + n;
@@ -332,7 +329,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
                 for (int j = 0; j < F::kCols; j++)
                     if (j < have) put(out + (size_t)j * p.out_stride, acc[j]);
             }
-        } else if (done) {
+        } else if (__all_sync(0xffffffffu, left > 0)) {
             // over the ring, all of whose copies and products are done: [token][row]
             float *part = reinterpret_cast<float *>(stages) + c0 * 128 + row;
 #pragma unroll
@@ -397,7 +394,7 @@ struct ManyParams {
     int T, N, KB, tiles_m, tiles_n;
     void *out;
     int32_t *err;
-    uint64_t timeout_ns;
+    uint32_t polls;                              // of a wait, at most
     int stall;
 };
 
@@ -431,8 +428,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     uint64_t *full = reinterpret_cast<uint64_t *>(boxes + 8 * kManyBoxes);
     uint64_t *empty = full + kManyStages, *acc_full = empty + kManyStages, *acc_empty = acc_full + 4, *stall_bar = acc_empty + 4, *drain_bar = stall_bar + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    const Bound bound{p.timeout_ns, abort_flag, p.err};
+    const Bound bound{p.polls, p.err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     const int tiles = p.tiles_m * p.tiles_n, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int mine = tiles > pair ? (tiles - 1 - pair) / pairs + 1 : 0, nq = mine * p.KB;
@@ -447,7 +443,6 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         }
         mbar_init(stall_bar, 1);
         mbar_init(drain_bar, 1);
-        *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) {
@@ -486,36 +481,33 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         // the last fill of each stage, the other CTA's part too, lands before the pair exits
         for (int s = 0; rank == 0 && s < kManyStages && s < q; s++) {
             const int last = q - 1 - ((q - 1 - s) % kManyStages);
-            if (!pipe::warp_wait(full + s, (last / kManyStages) & 1, p.timeout_ns) && lane == 0) atomicExch(p.err, MOE_ETIMEOUT);
+            wait(full + s, (last / kManyStages) & 1, bound);
         }
     } else if (warp == 9 && rank == 0) {
-        bool ok = true;
         if (elected()) {
+            int left = all_polls(p.polls, nq);
             Ring r;
-            for (int q = 0; q < nq && ok; q++, r.next(kManyStages)) {
-                const int s = r.at, k = 2 * (q & 1);
-                ok = wait(full + s, r.turn, bound);
-                const uint32_t at = saddr(stages + s * kManyStage);
+            for (int q = 0; q < nq; q++, r.next(kManyStages)) {
+                const int k = 2 * (q & 1);
+                wait_on<true>(full + r.at, r.turn, left);
+                const uint32_t at = saddr(stages + r.at * kManyStage);
                 const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    if (q >= 2) ok = ok && wait(acc_empty + k + h, ((q >> 1) - 1) & 1, bound);
-                    if (!ok) break;
+                    if (q >= 2) wait_on<true>(acc_empty + k + h, ((q >> 1) - 1) & 1, left);
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; kk++)
                         mma_e4m3<2>(tmem + (k + h) * 128, a + 2 * kk, b + (h * 64 * 128 >> 4) + 2 * kk, idesc_e4m3(256, 128), kk > 0);
                     commit_pair(acc_full + k + h);
                 }
-                if (ok) commit_pair(empty + s);
+                commit_pair(empty + r.at);
             }
+            commit_pair(drain_bar);
+            if (left <= 0) atomicExch(p.err, MOE_ETIMEOUT);
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {                           // what has been issued ends before the memory goes
-            if (lane == 0) commit_pair(drain_bar);
-            __syncwarp();
-            pipe::warp_wait(drain_bar, 0, p.timeout_ns);
-        }
+        __syncwarp();
+        wait(drain_bar, 0, bound);           // what has been issued ends before the memory goes
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManySumRegs));
@@ -529,8 +521,8 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         uint8_t *box = boxes + warp * kManyBoxes;
         const uint32_t free_bar = mapped(saddr(acc_empty), 0);
         int q = 0;
-        bool done = true;
-        for (int li = 0; li < mine && done; li++) {
+        int left = all_polls(p.polls, nq);
+        for (int li = 0; li < mine; li++) {
             int m, n;
             many_tile(p, pair + li * pairs, m, n);
             const int t = m * 256 + rank * 128 + (warp & 3) * 32 + lane, n0 = n * 256 + h * 128;
@@ -540,29 +532,26 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; j++) acc[j] = 0.0f;
-            float next_x = __ldg(sx), next_w = __ldg(sw);              // (their product waits for the loads: a block later)
-            for (int kb = 0; kb < p.KB && done; kb++, q++) {
+            // the scales are loaded a block ahead and multiplied when their block comes
+            float xs = __ldg(sx), ws = __ldg(sw);
+            for (int kb = 0; kb < p.KB; kb++, q++) {
                 const int k = 2 * (q & 1) + h;
-                const float scale = next_x * next_w;
-                if (kb + 1 < p.KB) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
-                done = __all_sync(0xffffffffu, wait(acc_full + k, (q >> 1) & 1, bound));
+                const float scale = xs * ws;
+                if (kb + 1 < p.KB) xs = __ldg(sx + kb + 1), ws = __ldg(sw + kb + 1);
+                wait_on<false>(acc_full + k, (q >> 1) & 1, left);
+                __syncwarp();
                 tc_fence_after();
-                if (done) {
-                    uint32_t d[2][16];
-                    tmem_ask(lanes + k * 128, d[0]);
 #pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        tmem_got(d[c & 1]);
-                        if (c < 7) tmem_ask(lanes + k * 128 + (c + 1) * 16, d[(c + 1) & 1]);
+                for (int c = 0; c < 128; c += 16) {
+                    uint32_t d[16];
+                    umma::tmem_ld_x16(lanes + k * 128 + c, d);
 #pragma unroll
-                        for (int j = 0; j < 16; j++) acc[16 * c + j] = fmaf(scale, __uint_as_float(d[c & 1][j]), acc[16 * c + j]);
-                    }
+                    for (int j = 0; j < 16; j++) acc[c + j] = fmaf(scale, __uint_as_float(d[j]), acc[c + j]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(free_bar + k * 8) : "memory");
             }
-            if (!done) break;
             // this warp's 32 x 128 results, in boxes of 128 bytes a row whose 16-byte
             // pieces stand as TMA's 128-byte swizzle has them (no bank conflicts)
             constexpr int PER = 128 / sizeof(O), ROUND = kManyBoxes / 4096;        // columns of a box; boxes at a time
@@ -604,6 +593,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     if (n0 + c >= whole && n0 + c < p.N) put(out + c, acc[c]);
             }
         }
+        if (left <= 0) atomicExch(p.err, MOE_ETIMEOUT);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
@@ -616,7 +606,9 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     }
 }
 
-// ---------------------------------------------------------------- host
+// A poll that fails takes some 50 ns, 32 of them asleep.
+uint32_t polls_of(uint64_t ns) { return (uint32_t)std::min<uint64_t>(ns / 50 + 1, INT32_MAX); }
+
 int encode_tile(CUtensorMap *m, const void *base, size_t rows, size_t cols, size_t stride, int box_rows) {
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {rows > 1 ? stride : align_up(cols, 16)};
     const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
@@ -637,7 +629,7 @@ int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd
     static OnDevices ready;
     const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kManySmem); });
     if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
-    const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / 256 + 1, q.out, q.err, q.timeout_ns, q.stall};
+    const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / 256 + 1, q.out, q.err, q.polls, q.stall};
     const int pairs = (int)std::min<int64_t>(num_sms() / 2, (int64_t)p.tiles_m * p.tiles_n);
     many_kernel<O><<<2 * pairs, kManyThreads, kManySmem, st>>>(xmap, wmap, omap, p);
     return check_launch("many_kernel");
@@ -727,7 +719,7 @@ extern "C" int moe_scaled_product(const moe_scaled_matrix_desc *wd, const void *
     ProductParams p = {};
     p.sx = x_scales, p.sw = wd->scales, p.sx_stride = x_scale_stride, p.sw_stride = wd->scale_stride, p.out_stride = out_stride;
     p.T = T, p.N = wd->N, p.KB = (int)blocks, p.out = out, p.err = static_cast<int32_t *>(ws);
-    p.timeout_ns = wait.timeout_ns ? wait.timeout_ns : pipe::kDefaultWaitNs, p.stall = wait.stall;
+    p.polls = polls_of(wait.timeout_ns ? wait.timeout_ns : pipe::kDefaultWaitNs), p.stall = wait.stall;
     return out_dtype == MOE_DTYPE_F32 ? launch_product<float>(x, x_stride, wd, p, stream)
                                       : launch_product<__nv_bfloat16>(x, x_stride, wd, p, stream);
 }
