@@ -9,7 +9,6 @@
 // block's two scales.  Nothing but the inner sum of 128 is left to the tensor
 // cores, and any fp32 scale is met exactly.
 #include <algorithm>
-#include <cstdlib>
 
 #include "e4m3.cuh"
 #include "gemm_umma.cuh"
@@ -141,7 +140,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *at, float v) { *at = __float2
 
 // ---------------------------------------------------------------- few tokens
 // The weights are the 128 rows of the MMA and the tokens its `nt` columns, so
-// that a tile of weights is read once, for a token as for 256.  A cluster of
+// that a tile of weights is read once, for a token as for 64.  A cluster of
 // `split` CTAs shares a tile's blocks of K and joins the sums through
 // distributed shared memory, in the order of its CTAs.
 constexpr int kFewMaxStages = 12;
@@ -150,8 +149,8 @@ template <int MAXN>
 struct Few {
     static constexpr int kSumWarps = MAXN >= 64 ? 8 : 4;            // four a half of the columns, or of all
     static constexpr int kCols = MAXN / (kSumWarps / 4);            // columns of a thread, at most
-    static constexpr int kSlots = MAXN <= 64 ? 4 : 2;               // accumulators
-    static constexpr int kTmem = kSlots * MAXN;                     // TMEM columns: 64 to 512
+    static constexpr int kSlots = 4;                                // accumulators
+    static constexpr int kTmem = kSlots * MAXN;                     // TMEM columns: 64 to 256
     static constexpr int kThreads = 32 * (kSumWarps + 2);           // and a warp for TMA, one for the MMAs
 };
 
@@ -179,24 +178,37 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     const Bound bound{p.polls, p.err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S, t0 = blockIdx.y * NT;
+    const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S, t0 = 0;
     const int kb0 = (int)((int64_t)p.KB * rank / S), nkb = (int)((int64_t)p.KB * (rank + 1) / S) - kb0;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; s++) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, 1);
-        }
-        for (int k = 0; k < F::kSlots; k++) {
-            mbar_init(acc_full + k, 1);
-            mbar_init(acc_empty + k, F::kSumWarps);
-        }
-        mbar_init(stall_bar, 1);
-        mbar_init(drain_bar, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    const int fills = min(nkb, p.stages);
     if (warp == F::kSumWarps) {
-        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
-        if (lane == 1) asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+        // The first fills at once, a lane for each copy, before the CTA has come
+        // together: the barriers that they tell are this warp's own work.
+        if (lane < p.stages) {
+            mbar_init(full + lane, 1);
+            mbar_init(empty + lane, 1);
+        }
+        if (lane < F::kSlots) {
+            mbar_init(acc_full + lane, 1);
+            mbar_init(acc_empty + lane, F::kSumWarps);
+        }
+        if (lane == 0) {
+            mbar_init(stall_bar, 1);
+            mbar_init(drain_bar, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane < 2 * fills) {
+            const int q = lane >> 1;
+            uint8_t *stage = stages + (size_t)q * stage_bytes;
+            if (lane & 1) {
+                pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + q);
+            } else {
+                mbar_expect_tx(full + q, stage_bytes);
+                pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + q);
+            }
+        }
     }
     if (warp == F::kSumWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)), "n"(F::kTmem) : "memory");
@@ -208,20 +220,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
     const uint32_t tmem = *tmem_holder;
 
     if (warp == F::kSumWarps) {
-        // the first fills all at once, a lane for each copy
-        const int n0 = min(nkb, p.stages);
-        if (lane < 2 * n0) {
-            const int q = lane >> 1;
-            uint8_t *stage = stages + (size_t)q * stage_bytes;
-            if (lane & 1) {
-                pipe::tma_2d(stage + 128 * 128, &xmap, (kb0 + q) * 128, t0, full + q);
-            } else {
-                mbar_expect_tx(full + q, stage_bytes);
-                pipe::tma_2d(stage, &wmap, (kb0 + q) * 128, tile * 128, full + q);
-            }
-        }
-        __syncwarp();
-        int q = n0;
+        int q = fills;
         if (elected()) {
             Ring r;
             for (; q < nkb; q++, r.next(p.stages)) {
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         wait(drain_bar, 0, bound);           // what has been issued ends before the memory goes
     } else {
         const int tid = threadIdx.x, row = tid & 127;
-        if (p.stall && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {        // test hook: bytes that no copy sends
+        if (p.stall && blockIdx.x == 0 && warp == 0) {        // test hook: bytes that no copy sends
             if (lane == 0) mbar_expect_tx(stall_bar, 16);
             __syncwarp();
             wait(stall_bar, 0, bound);
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
         // this warp's columns: from c0, nc of them (a multiple of 16)
         const int half = F::kSumWarps == 8 ? (NT / 16 + 1) / 2 * 16 : NT;
         const int c0 = F::kSumWarps == 8 && warp >= 4 ? half : 0, nc = min(half, NT - c0);
-        constexpr int NC = F::kCols < 32 || F::kCols > 64 ? 16 : 32;          // (32 beside 128 sums do not fit the registers)
+        constexpr int NC = F::kCols < 32 ? 16 : 32;
         float acc[F::kCols];
 #pragma unroll
         for (int j = 0; j < F::kCols; j++) acc[j] = 0.0f;
@@ -377,15 +376,20 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
 // fill TMEM, each in two halves that are multiplied, read and freed by themselves (an accumulator's turn,
 // from one block's products to the next one's, is the shorter); eight warps keep 128 sums a thread.  Persistent over the tiles,
 // eight rows of tiles at a time, so that the tiles in work share what L2 holds.
-constexpr int kManyStages = 5;
-constexpr int kManyStage = 2 * 128 * 128;
+template <int TILE>                       // outputs of a tile: 256 or 128
+struct Many {
+    static constexpr int kParts = TILE / 128;                // an MMA's outputs are 128
+    static constexpr int kDepth = 512 / TILE;                // accumulators
+    static constexpr int kStage = (128 + TILE / 2) * 128;
+    static constexpr int kStages = TILE == 256 ? 5 : 6;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + 8 * 8192 + (2 * kStages + 2 * 4 + 2) * 8 + 16;
+};
+constexpr int kManyBoxes = 8192;         // staging of a warp's results
 constexpr int kManyThreads = 384;        // warps 0-7 sums, 8 TMA, 9 MMA (of the pair's first CTA); 10 and 11 fill the warpgroup
-// Registers: 168 a thread at launch; 256 threads with 128 sums take 208, the
+// Registers: 168 a thread at launch; 256 threads with up to 128 sums take 208, the
 // other 128 keep 72: 256 * 208 + 128 * 72 <= 384 * 168.
 constexpr int kManySumRegs = 208, kManyOtherRegs = 72;
 static_assert(256 * kManySumRegs + 128 * kManyOtherRegs <= 384 * 168 && kManyThreads == 384, "within the launch's registers");
-constexpr int kManyBoxes = 8192;         // staging of a warp's results
-constexpr size_t kManySmem = 1024 + kManyStages * kManyStage + 8 * kManyBoxes + (2 * kManyStages + 10) * 8 + 16;
 constexpr int kManyRows = 8;             // rows of tiles that go together
 
 struct ManyParams {
@@ -419,27 +423,29 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *m, const void *src,
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(saddr(src)) : "memory");
 }
 
-template <typename O>
+template <int TILE, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
 many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap, const ManyParams p) {
+    using M = Many<TILE>;
+    constexpr int H = TILE / 2, P = M::kParts, D = M::kDepth;        // H: outputs of a warp
     extern __shared__ __align__(1024) uint8_t smdyn[];
     uint8_t *stages = smdyn + ((1024u - (saddr(smdyn) & 1023u)) & 1023u);
-    uint8_t *boxes = stages + kManyStages * kManyStage;
+    uint8_t *boxes = stages + M::kStages * M::kStage;
     uint64_t *full = reinterpret_cast<uint64_t *>(boxes + 8 * kManyBoxes);
-    uint64_t *empty = full + kManyStages, *acc_full = empty + kManyStages, *acc_empty = acc_full + 4, *stall_bar = acc_empty + 4, *drain_bar = stall_bar + 1;
+    uint64_t *empty = full + M::kStages, *acc_full = empty + M::kStages, *acc_empty = acc_full + 4, *stall_bar = acc_empty + 4, *drain_bar = stall_bar + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     const Bound bound{p.polls, p.err};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     const int tiles = p.tiles_m * p.tiles_n, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int mine = tiles > pair ? (tiles - 1 - pair) / pairs + 1 : 0, nq = mine * p.KB;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kManyStages; s++) {
+        for (int s = 0; s < M::kStages; s++) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
         for (int k = 0; k < 4; k++) {
             mbar_init(acc_full + k, 1);
-            mbar_init(acc_empty + k, 8);
+            mbar_init(acc_empty + k, 16 / P);
         }
         mbar_init(stall_bar, 1);
         mbar_init(drain_bar, 1);
@@ -463,14 +469,15 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         if (elected()) {
             const uint32_t first_full = mapped(saddr(full), 0);
             Ring r;
-            for (; q < nq; q++, r.next(kManyStages)) {
-                uint8_t *stage = stages + r.at * kManyStage;
-                if (q >= kManyStages && !wait(empty + r.at, r.turn ^ 1, bound)) break;
+            for (; q < nq; q++, r.next(M::kStages)) {
+                uint8_t *stage = stages + r.at * M::kStage;
+                if (q >= M::kStages && !wait(empty + r.at, r.turn ^ 1, bound)) break;
                 const uint32_t bar = first_full + r.at * 8;
-                if (rank == 0) mbar_expect_tx(full + r.at, 2 * kManyStage);
+                if (rank == 0) mbar_expect_tx(full + r.at, 2 * M::kStage);
                 tma_pair(stage, &xmap, kb * 128, m * 256 + rank * 128, bar);
-                tma_pair(stage + 128 * 128, &wmap, kb * 128, n * 256 + rank * 64, bar);
-                tma_pair(stage + 192 * 128, &wmap, kb * 128, n * 256 + 128 + rank * 64, bar);
+#pragma unroll
+                for (int h = 0; h < P; h++)
+                    tma_pair(stage + (128 + h * 64) * 128, &wmap, kb * 128, n * TILE + h * 128 + rank * 64, bar);
                 if (++kb == p.KB) {
                     kb = 0;
                     if (++li < mine) many_tile(p, pair + li * pairs, m, n);
@@ -479,22 +486,22 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         }
         q = __reduce_max_sync(0xffffffffu, (unsigned)q);
         // the last fill of each stage, the other CTA's part too, lands before the pair exits
-        for (int s = 0; rank == 0 && s < kManyStages && s < q; s++) {
-            const int last = q - 1 - ((q - 1 - s) % kManyStages);
-            wait(full + s, (last / kManyStages) & 1, bound);
+        for (int s = 0; rank == 0 && s < M::kStages && s < q; s++) {
+            const int last = q - 1 - ((q - 1 - s) % M::kStages);
+            wait(full + s, (last / M::kStages) & 1, bound);
         }
     } else if (warp == 9 && rank == 0) {
         if (elected()) {
             int left = all_polls(p.polls, nq);
             Ring r;
-            for (int q = 0; q < nq; q++, r.next(kManyStages)) {
-                const int k = 2 * (q & 1);
+            for (int q = 0; q < nq; q++, r.next(M::kStages)) {
+                const int k = P * (q % D);
                 wait_on<true>(full + r.at, r.turn, left);
-                const uint32_t at = saddr(stages + r.at * kManyStage);
+                const uint32_t at = saddr(stages + r.at * M::kStage);
                 const uint64_t a = sw128_desc(at), b = sw128_desc(at + 128 * 128);
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    if (q >= 2) wait_on<true>(acc_empty + k + h, ((q >> 1) - 1) & 1, left);
+                for (int h = 0; h < P; h++) {
+                    if (q >= D) wait_on<true>(acc_empty + k + h, (q / D - 1) & 1, left);
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; kk++)
@@ -525,26 +532,26 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         for (int li = 0; li < mine; li++) {
             int m, n;
             many_tile(p, pair + li * pairs, m, n);
-            const int t = m * 256 + rank * 128 + (warp & 3) * 32 + lane, n0 = n * 256 + h * 128;
+            const int t = m * 256 + rank * 128 + (warp & 3) * 32 + lane, n0 = n * TILE + h * H;
             // rows behind the end have scales of 0, columns those of the last block
             const float *sx = p.sx + (size_t)min(t, p.T - 1) * p.sx_stride;
             const float *sw = p.sw + (size_t)min(n0 >> 7, (p.N - 1) >> 7) * p.sw_stride;
-            float acc[128];
+            float acc[H];
 #pragma unroll
-            for (int j = 0; j < 128; j++) acc[j] = 0.0f;
+            for (int j = 0; j < H; j++) acc[j] = 0.0f;
             // the scales are loaded a block ahead and multiplied when their block comes
             float xs = __ldg(sx), ws = __ldg(sw);
             for (int kb = 0; kb < p.KB; kb++, q++) {
-                const int k = 2 * (q & 1) + h;
+                const int k = P * (q % D) + (P == 2 ? h : 0);
                 const float scale = xs * ws;
                 if (kb + 1 < p.KB) xs = __ldg(sx + kb + 1), ws = __ldg(sw + kb + 1);
-                wait_on<false>(acc_full + k, (q >> 1) & 1, left);
+                wait_on<false>(acc_full + k, (q / D) & 1, left);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < H; c += 16) {
                     uint32_t d[16];
-                    umma::tmem_ld_x16(lanes + k * 128 + c, d);
+                    umma::tmem_ld_x16(lanes + k * 128 + (P == 2 ? 0 : h * H) + c, d);
 #pragma unroll
                     for (int j = 0; j < 16; j++) acc[c + j] = fmaf(scale, __uint_as_float(d[j]), acc[c + j]);
                 }
@@ -554,11 +561,11 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             }
             // this warp's 32 x 128 results, in boxes of 128 bytes a row whose 16-byte
             // pieces stand as TMA's 128-byte swizzle has them (no bank conflicts)
-            constexpr int PER = 128 / sizeof(O), ROUND = kManyBoxes / 4096;        // columns of a box; boxes at a time
+            constexpr int PER = 128 / sizeof(O), ROUND = H / PER < 2 ? 1 : 2;        // columns of a box; boxes at a time
             const int whole = p.N & ~(16 / (int)sizeof(O) - 1);
             const int t_warp = t - lane;
 #pragma unroll
-            for (int c = 0; c < 128; c += PER * ROUND) {
+            for (int c = 0; c < H; c += PER * ROUND) {
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
 #pragma unroll
@@ -586,10 +593,10 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 }
             }
             // TMA writes whole 16-byte pieces: what is left of the rows goes by itself
-            if (whole < p.N && n0 < p.N && n0 + 128 > whole && t < p.T) {
+            if (whole < p.N && n0 < p.N && n0 + H > whole && t < p.T) {
                 O *out = static_cast<O *>(p.out) + (size_t)t * p.out_stride + n0;
 #pragma unroll
-                for (int c = 0; c < 128; c++)
+                for (int c = 0; c < H; c++)
                     if (n0 + c >= whole && n0 + c < p.N) put(out + c, acc[c]);
             }
         }
@@ -606,6 +613,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     }
 }
 
+// ---------------------------------------------------------------- host
 // A poll that fails takes some 50 ns, 32 of them asleep.
 uint32_t polls_of(uint64_t ns) { return (uint32_t)std::min<uint64_t>(ns / 50 + 1, INT32_MAX); }
 
@@ -617,7 +625,7 @@ int encode_tile(CUtensorMap *m, const void *base, size_t rows, size_t cols, size
 
 int no_map() { return fail(MOE_ECUDA, "scaled_product: no tensor map"); }
 
-template <typename O>
+template <int TILE, typename O>
 int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, const ProductParams &q, cudaStream_t st) {
     CUtensorMap xmap, wmap, omap;
     const cuuint64_t dims[2] = {std::max<cuuint64_t>(16 / sizeof(O), q.N / (16 / sizeof(O)) * (16 / sizeof(O))), (cuuint64_t)q.T}, strides[1] = {(q.T > 1 ? q.out_stride : align_up(q.N, 8)) * sizeof(O)};
@@ -627,11 +635,11 @@ int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return no_map();
     static OnDevices ready;
-    const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kManySmem); });
+    const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<TILE, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Many<TILE>::kSmem); });
     if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
-    const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / 256 + 1, q.out, q.err, q.polls, q.stall};
+    const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / TILE + 1, q.out, q.err, q.polls, q.stall};
     const int pairs = (int)std::min<int64_t>(num_sms() / 2, (int64_t)p.tiles_m * p.tiles_n);
-    many_kernel<O><<<2 * pairs, kManyThreads, kManySmem, st>>>(xmap, wmap, omap, p);
+    many_kernel<TILE, O><<<2 * pairs, kManyThreads, Many<TILE>::kSmem, st>>>(xmap, wmap, omap, p);
     return check_launch("many_kernel");
 }
 
@@ -639,16 +647,19 @@ template <int MAXN, typename O>
 int launch_few(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, ProductParams p, cudaStream_t st) {
     CUtensorMap wmap, xmap;
     if (encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 128) || encode_tile(&xmap, x, p.T, wd->K, x_stride, p.nt)) return no_map();
-    const int tiles = (p.N - 1) / 128 + 1, cols = (p.T - 1) / p.nt + 1;
+    const int tiles = (p.N - 1) / 128 + 1;
+    // Up to two CTAs an SM, and with more than 32 tokens four blocks a CTA: the
+    // join goes over all its tokens (64 of 2560 x 2048: 7.2 us with four CTAs a tile, 8.5 with eight;
+    // one of 5120 x 4096: 8.2 with four, 9.1 with two).
     p.split = 1;
-    while (p.split < 8 && 2 * p.split <= p.KB && (int64_t)tiles * cols * p.split * 2 <= (p.nt <= 128 ? 2 : 1) * num_sms()) p.split *= 2;
-    const int stage = few_stage(p.nt), least = std::max(2, p.split > 1 ? (p.nt * 512 + stage - 1) / stage : 2);      // room for the sums
-    p.stages = std::max(least, std::min({few_share(p.KB, p.split), kFewMaxStages, (MAXN <= 128 ? 100 << 10 : 160 << 10) / stage}));
+    while (p.split < 8 && 2 * p.split * (p.nt > 32 ? 4 : 1) <= p.KB && (int64_t)tiles * p.split * 2 <= 2 * num_sms()) p.split *= 2;
+    const int stage = few_stage(p.nt), least = p.split > 1 ? std::max(2, (p.nt * 512 + stage - 1) / stage) : 2;      // room for the sums
+    p.stages = std::max(least, std::min({few_share(p.KB, p.split), kFewMaxStages, (100 << 10) / stage}));
     static OnDevices ready;
     cudaError_t e = ready.once([] { return cudaFuncSetAttribute(few_kernel<MAXN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10); });
     if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.split), (unsigned)cols);
+    cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(Few<MAXN>::kThreads);
     cfg.dynamicSmemBytes = few_smem<MAXN>(p.KB, p.split, p.stages, p.nt);
     cfg.stream = st;
@@ -665,17 +676,21 @@ int launch_few(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd,
 
 template <typename O>
 int launch_product(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, ProductParams p, cudaStream_t st) {
-    // Tokens in one row of tiles, or as many rows as the SMs take at a time.
-    const int64_t tiles = (p.N - 1) / 128 + 1;
-    const char *force = getenv("MANY");
-    if (force ? atoi(force) : p.T > 1024) return launch_many<O>(x, x_stride, wd, p, st);
-    int64_t rows = std::max<int64_t>((p.T - 1) / 256 + 1, std::min<int64_t>(num_sms() / tiles, (p.T - 1) / 128 + 1));
-    p.nt = (int)(((p.T - 1) / rows + 1 + 15) / 16 * 16);
-    if (p.nt <= 16) return launch_few<16, O>(x, x_stride, wd, p, st);
-    if (p.nt <= 32) return launch_few<32, O>(x, x_stride, wd, p, st);
-    if (p.nt <= 64) return launch_few<64, O>(x, x_stride, wd, p, st);
-    if (p.nt <= 128) return launch_few<128, O>(x, x_stride, wd, p, st);
-    return launch_few<256, O>(x, x_stride, wd, p, st);
+    // A kernel by the tokens: with 64 the first takes 11.2 us at 5120 x 4096, pairs
+    // 13.2; with 96 its 128 columns took 19.5, pairs 13.4.
+    if (p.T <= 64) {
+        p.nt = (p.T + 15) / 16 * 16;
+        if (p.nt <= 16) return launch_few<16, O>(x, x_stride, wd, p, st);
+        if (p.nt <= 32) return launch_few<32, O>(x, x_stride, wd, p, st);
+        return launch_few<64, O>(x, x_stride, wd, p, st);
+    }
+    // Pairs' tiles by the rounds that the grid takes over them, a round of 128 outputs
+    // for five eighths of one of 256 (32 blocks of K: 9.9 and 16.0 us): 256 tokens of 5120 x 4096
+    // take 13.7 us in tiles of 128 and 17.8 in tiles of 256, 2048 of 4096 x 4096 39.3 and 32.0.
+    const int64_t pairs = std::max(1, num_sms() / 2), rows = (p.T - 1) / 256 + 1;
+    auto rounds = [&](int64_t tile) { return (rows * ((p.N - 1) / tile + 1) + pairs - 1) / pairs; };
+    if (rounds(128) * ((int64_t)p.KB + 1) >= INT32_MAX) return fail(MOE_EUNSUPPORTED, "scaled_product: T=%d N=%d K=%d", p.T, p.N, wd->K);
+    return 5 * rounds(128) < 8 * rounds(256) ? launch_many<128, O>(x, x_stride, wd, p, st) : launch_many<256, O>(x, x_stride, wd, p, st);
 }
 
 int check_matrix(const moe_scaled_matrix_desc *wd, const char *who) {
