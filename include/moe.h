@@ -403,8 +403,8 @@ int moe_paged_attention(const moe_kv_desc *kv, const void *q, int q_dtype, size_
 
 /* x [rows][cols] (F32 or BF16) by blocks of block_rows (1: activations, 128:
  * weights) x 128.  Rows x_stride / code_stride elements apart (16-byte
- * multiples; anything for a single row); at most 2^31 - 1 spans of 256 columns,
- * and 65535 * 128 rows with block_rows 128.  Outputs overlap nothing. */
+ * multiples; anything for a single row); at most 2^30 columns,
+ * fewer than 2 10^9 spans of 512 of them, and with block_rows 128 at most 65535 * 128 rows.  Outputs overlap nothing. */
 int moe_quantise_e4m3(const void *x, int x_dtype, size_t x_stride, int rows, int cols,
                       int block_rows, int pow2, void *codes, size_t code_stride, float *scales,
                       size_t scale_stride, cudaStream_t stream);

@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -89,17 +90,29 @@ __device__ __forceinline__ float2 inverses(float scale) {
 // Numbers 8 c .. 8 c + 7 of a row of n at a 16-byte boundary, zeros behind its
 // end: what stands there is neither read nor written.
 template <typename X>
-__device__ __forceinline__ Floats8 row_load8(const X *row, int c, int n) {
+struct Raw8 {
+    uint4 w[sizeof(X) / 2];
+    __device__ __forceinline__ Floats8 floats() const { return floats8<X>(w); }
+};
+template <typename X>
+__device__ __forceinline__ Raw8<X> row_load8(const X *row, int c, int n) {
+    Raw8<X> raw;
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(X) / 2; j++) raw.w[j] = make_uint4(0, 0, 0, 0);
     if (8 * c + 8 <= n) {
-        uint4 raw[sizeof(X) / 2];
 #pragma unroll
-        for (int j = 0; j < (int)sizeof(X) / 2; j++) raw[j] = reinterpret_cast<const uint4 *>(row + 8 * (size_t)c)[j];
-        return floats8<X>(raw);
+        for (int j = 0; j < (int)sizeof(X) / 2; j++) raw.w[j] = reinterpret_cast<const uint4 *>(row + 8 * (size_t)c)[j];
+    } else if (8 * c < n) {
+        using Bits = std::conditional_t<sizeof(X) == 2, uint16_t, uint32_t>;
+        const Bits *at = reinterpret_cast<const Bits *>(row + 8 * (size_t)c);
+        uint32_t u[2 * sizeof(X)] = {};
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (8 * c + j < n) u[j * sizeof(X) / 4] |= (uint32_t)at[j] << (sizeof(X) == 2 ? 16 * (j & 1) : 0);
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(X) / 2; j++) raw.w[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
     }
-    Floats8 f;
-#pragma unroll
-    for (int j = 0; j < 8; j++) f.x[j] = 8 * c + j < n ? (float)row[8 * (size_t)c + j] : 0.0f;
-    return f;
+    return raw;
 }
 
 __device__ __forceinline__ void row_store8(float *row, int c, int n, const float *f) {
@@ -139,6 +152,27 @@ __device__ __forceinline__ void row_store8(uint8_t *row, int c, int n, uint2 w) 
 }
 
 // ---------------------------------------------------------------- scales
+// Eight codes of a block: x / scale rounded to fp32, then to e4m3.  A power of two
+// divides exactly, by one product.  Else the quotient comes from the rounded
+// reciprocal inv: q = x inv, its remainder r = x - q scale, exact in an fma, and
+// q + r inv, which rounds as the quotient does (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990); with a
+// scale of 2^-100 to 2^120 nothing underflows that an e4m3 border depends on.
+// (Two products that bracket the quotient and a division where they differ, as
+// the cache's append has it, cost more here: numbers of bf16 over a scale out of
+// bf16 fall on the middle of two codes often.  16381 x 4096: 65 us, this way 46.)
+__device__ __forceinline__ uint2 block_codes(const float *f, float scale, bool pow2) {
+    if (pow2) return e4m3x8(f, __uint_as_float(0x7f000000u - __float_as_uint(scale)));       // (NaN from NaN: 0xff000001)
+    const float inv = __fdiv_rn(1.0f, scale);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float q = __fmul_rn(f[j], inv);
+        y[j] = fmaf(fmaf(-q, scale, f[j]), inv, q);
+    }
+    return e4m3x8(y, 1.0f);
+}
+
 constexpr int kScaleBlock = 128;          // columns of a block
 
 // The largest size of eight numbers, as its bits: they order as the sizes do,

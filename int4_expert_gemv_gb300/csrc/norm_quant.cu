@@ -3,7 +3,7 @@
 //
 // Norm.  h = x + res;  y = h / sqrt(mean(h^2) + eps) * w, everything in fp32
 // from numbers read once: a row stays in the registers of the threads that
-// have loaded it (8 to 64 numbers each), so that the sum of squares,
+// have loaded it (8 to 32 numbers each), so that the sum of squares,
 // the block's largest size and the result need no second read.  In 8 bits a
 // block of 128 numbers belongs to 16 neighbouring lanes, which find its
 // largest size by shuffles.
@@ -18,7 +18,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxNormWidth = 32768;      // 512 threads of 64 numbers
+constexpr int kMaxCols = 1 << 30;         // of a quantised row
+constexpr int kNoChunk = kMaxCols / 8;    // behind every row
+constexpr int kMaxNormWidth = 32768;      // 1024 threads of 32 numbers
 
 struct NormParams {
     const void *x, *res, *w;
@@ -30,93 +32,106 @@ struct NormParams {
     bool pow2;
 };
 
-// The largest of the 16 lanes that hold a block.
-__device__ __forceinline__ uint32_t most_of_16(uint32_t m) {
+// The largest of the lanes that hold a block.
+template <int LANES>
+__device__ __forceinline__ uint32_t most_of(uint32_t m) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
 
 // X, R: types of x and res (R = void: no residual); Y: type of y (uint8_t:
 // e4m3 codes).  A row belongs to a warp (ROWS warps, each with a row of its
 // own) or, for ROWS = 1, to the CTA; each thread has NV chunks of 8 numbers.
+// Persistent: the next row is on its way while this one is computed.
 template <typename X, typename R, typename Y, int NV, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : 512) norm_kernel(const NormParams p) {
-    constexpr bool RES = !std::is_void<R>::value;
+__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : NV == 1 ? 256 : 1024) norm_kernel(const NormParams p) {
+    constexpr bool RES = !std::is_void<R>::value, AHEAD = NV < 4;      // (32 numbers and the next 32 do not fit 1024 threads' registers)
     using RT = std::conditional_t<RES, R, float>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = ROWS > 1 ? blockIdx.x * ROWS + warp : blockIdx.x;
+    __shared__ float part[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int first = ROWS > 1 ? lane : threadIdx.x, step = ROWS > 1 ? 32 : blockDim.x;
-    if (ROWS > 1 && t >= p.T) return;
-    const X *x = static_cast<const X *>(p.x) + (size_t)t * p.x_stride;
-    const RT *res = RES ? static_cast<const RT *>(p.res) + (size_t)t * p.res_stride : nullptr;
-    float h[NV][8];
-    float ss = 0.0f;
+    Raw8<X> a[NV];
+    Raw8<RT> b[NV];
+    auto load = [&](int64_t t) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const Floats8 a = row_load8<X>(x, first + i * step, p.d);
-        Floats8 b;
-        if (RES) b = row_load8<RT>(res, first + i * step, p.d);
-#pragma unroll
-        for (int j = 0; j < 8; j++) h[i][j] = RES ? a.x[j] + b.x[j] : a.x[j];
-    }
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        if (RES && p.sum && 8 * (first + i * step) < p.d)
-            row_store8(static_cast<RT *>(p.sum) + (size_t)t * p.sum_stride, first + i * step, p.d, h[i]);
-#pragma unroll
-        for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
-    }
-    ss = warp_sum(ss, 32);
-    if (ROWS == 1 && blockDim.x > 32) {
-        __shared__ float part[32];
-        if (lane == 0) part[warp] = ss;
-        __syncthreads();
-        ss = warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f, 32);
-    }
-    const float by = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.d) + p.eps));
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int c = first + i * step;
-        const bool in = 8 * c < p.d;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = h[i][j] * by;
-        if (p.w && in) {
-            const Floats8 w = p.w_bf16 ? row_load8<__nv_bfloat16>(static_cast<const __nv_bfloat16 *>(p.w), c, p.d)
-                                       : row_load8<float>(static_cast<const float *>(p.w), c, p.d);
-#pragma unroll
-            for (int j = 0; j < 8; j++) y[j] *= w.x[j];
+        for (int i = 0; i < NV; i++) {
+            a[i] = row_load8<X>(static_cast<const X *>(p.x) + (size_t)t * p.x_stride, first + i * step, p.d);
+            if (RES) b[i] = row_load8<RT>(static_cast<const RT *>(p.res) + (size_t)t * p.res_stride, first + i * step, p.d);
         }
-        if constexpr (sizeof(Y) == 1) {
-            const float scale = block_scale(most_of_16(in ? most8(y) : 0u), p.pow2);
-            if (in) {
-                row_store8(static_cast<uint8_t *>(p.y) + (size_t)t * p.y_stride, c, p.d, e4m3_quotients(y, scale, inverses(scale)));
-                if (c % 16 == 0) p.scales[(size_t)t * p.scale_stride + c / 16] = scale;
+    };
+    const int64_t rows = (int64_t)gridDim.x * ROWS;
+    int64_t t = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? warp : 0);
+    if (AHEAD && t < p.T) load(t);
+    for (int odd = 0; t < p.T; t += rows, odd ^= 1) {
+        float h[NV][8];
+        float ss = 0.0f;
+        if (!AHEAD) load(t);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const Floats8 u = a[i].floats(), v = RES ? b[i].floats() : u;
+#pragma unroll
+            for (int j = 0; j < 8; j++) h[i][j] = RES ? u.x[j] + v.x[j] : u.x[j];
+        }
+        if (AHEAD && t + rows < p.T) load(t + rows);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (RES && p.sum && 8 * (first + i * step) < p.d)
+                row_store8(static_cast<RT *>(p.sum) + (size_t)t * p.sum_stride, first + i * step, p.d, h[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
+        }
+        ss = warp_sum(ss, 32);
+        if (ROWS == 1 && warps > 1) {
+            if (lane == 0) part[odd][warp] = ss;          // (two sets: a row's are read before the next but one's are written)
+            __syncthreads();
+            ss = warp_sum(lane < warps ? part[odd][lane] : 0.0f, 32);
+        }
+        const float by = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.d) + p.eps));
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = first + i * step;
+            const bool in = 8 * c < p.d;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[j] = h[i][j] * by;
+            if (p.w && in) {
+                const Floats8 w = p.w_bf16 ? row_load8<__nv_bfloat16>(static_cast<const __nv_bfloat16 *>(p.w), c, p.d).floats()
+                                           : row_load8<float>(static_cast<const float *>(p.w), c, p.d).floats();
+#pragma unroll
+                for (int j = 0; j < 8; j++) y[j] *= w.x[j];
             }
-        } else if (in) {
-            row_store8(static_cast<Y *>(p.y) + (size_t)t * p.y_stride, c, p.d, y);
+            if constexpr (sizeof(Y) == 1) {
+                const float scale = block_scale(most_of<16>(in ? most8(y) : 0u), p.pow2);
+                if (in) {
+                    row_store8(static_cast<uint8_t *>(p.y) + (size_t)t * p.y_stride, c, p.d, block_codes(y, scale, p.pow2));
+                    if (c % 16 == 0) p.scales[(size_t)t * p.scale_stride + c / 16] = scale;
+                }
+            } else if (in) {
+                row_store8(static_cast<Y *>(p.y) + (size_t)t * p.y_stride, c, p.d, y);
+            }
         }
     }
+}
+
+// A CTA for a row of each SM's share while they last.
+template <typename F>
+int norm_grid(F kernel, int threads, int64_t rows) {
+    int ctas = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, 0) != cudaSuccess || ctas < 1) ctas = 1;
+    return (int)std::min<int64_t>(rows, (int64_t)ctas * num_sms());
 }
 
 template <typename X, typename R, typename Y>
 int launch_norm(const NormParams &p, cudaStream_t st) {
     const int chunks = (p.d + 7) / 8;
     auto threads = [&](int nv) { return ((chunks + nv - 1) / nv + 31) / 32 * 32; };
-    if (chunks <= 64) {
-        const unsigned grid = (unsigned)((p.T + (int64_t)3) / 4);
-        if (chunks <= 32) norm_kernel<X, R, Y, 1, 4><<<grid, 128, 0, st>>>(p);
-        else norm_kernel<X, R, Y, 2, 4><<<grid, 128, 0, st>>>(p);
-    } else if (threads(1) <= 256) {
-        norm_kernel<X, R, Y, 1, 1><<<p.T, threads(1), 0, st>>>(p);
-    } else if (threads(2) <= 512) {
-        norm_kernel<X, R, Y, 2, 1><<<p.T, threads(2), 0, st>>>(p);
-    } else if (threads(4) <= 512) {
-        norm_kernel<X, R, Y, 4, 1><<<p.T, threads(4), 0, st>>>(p);
-    } else {
-        norm_kernel<X, R, Y, 8, 1><<<p.T, threads(8), 0, st>>>(p);
-    }
+    auto go = [&](auto kernel, int n, int64_t rows) { kernel<<<norm_grid(kernel, n, rows), n, 0, st>>>(p); };
+    if (chunks <= 32) go(norm_kernel<X, R, Y, 1, 4>, 128, (p.T + (int64_t)3) / 4);
+    else if (chunks <= 64) go(norm_kernel<X, R, Y, 2, 4>, 128, (p.T + (int64_t)3) / 4);
+    else if (threads(1) <= 256 && p.T <= 8 * num_sms()) go(norm_kernel<X, R, Y, 1, 1>, threads(1), p.T);
+    else if (threads(2) <= 1024) go(norm_kernel<X, R, Y, 2, 1>, threads(2), p.T);
+    else go(norm_kernel<X, R, Y, 4, 1>, threads(4), p.T);
     return check_launch("norm_kernel");
 }
 
@@ -142,22 +157,42 @@ struct QuantParams {
     uint8_t *codes;
     float *scales;
     bool pow2;
-    FastDiv pairs;                                   // two blocks of a row: a warp's
+    FastDiv quads;                                   // four blocks of a row: a warp's
 };
 
+// A warp's unit is four blocks of a row, 16 numbers a lane (a block's scale costs
+// its lanes two divisions each, so that 8 numbers a lane took 50 us at 16381 x 4096);
+// U units are on their way at a time.
 template <typename X>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n = (int64_t)p.rows * p.pairs.d, step = (int64_t)gridDim.x * 8;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += step) {
-        const int r = p.pairs.div((int)u), c = ((int)u - r * p.pairs.d) * 32 + lane;
-        const bool in = 8 * c < p.cols;
-        Floats8 f = {};
-        if (in) f = row_load8<X>(static_cast<const X *>(p.x) + (size_t)r * p.x_stride, c, p.cols);
-        const float scale = block_scale(most_of_16(most8(f.x)), p.pow2);
-        if (in) {
-            row_store8(p.codes + (size_t)r * p.code_stride, c, p.cols, e4m3_quotients(f.x, scale, inverses(scale)));
-            if (c % 16 == 0) p.scales[(size_t)r * p.scale_stride + c / 16] = scale;
+    constexpr int U = sizeof(X) == 2 ? 2 : 1;
+    const int lane = threadIdx.x & 31, n = p.rows * p.quads.d, step = gridDim.x * 8;           // (the host keeps n + U step within 2^31)
+    for (int u0 = blockIdx.x * 8 + (threadIdx.x >> 5); u0 < n; u0 += U * step) {
+        Raw8<X> raw[U][2];
+        int r[U], c[U];
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            const int u = min(u0 + j * step, n - 1);
+            r[j] = p.quads.div(u);
+            c[j] = u0 + j * step < n ? (u - r[j] * p.quads.d) * 64 + 2 * lane : kNoChunk;
+#pragma unroll
+            for (int i = 0; i < 2; i++) raw[j][i] = row_load8<X>(static_cast<const X *>(p.x) + (size_t)r[j] * p.x_stride, c[j] + i, p.cols);
+        }
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            const Floats8 f = raw[j][0].floats(), g = raw[j][1].floats();
+            const float scale = block_scale(most_of<8>(max(most8(f.x), most8(g.x))), p.pow2);
+            if (8 * c[j] < p.cols) {
+                uint8_t *row = p.codes + (size_t)r[j] * p.code_stride;
+                const uint2 a = block_codes(f.x, scale, p.pow2), b = block_codes(g.x, scale, p.pow2);
+                if (8 * c[j] + 16 <= p.cols) {
+                    *reinterpret_cast<uint4 *>(row + 8 * (size_t)c[j]) = make_uint4(a.x, a.y, b.x, b.y);
+                } else {
+                    row_store8(row, c[j], p.cols, a);
+                    if (8 * c[j] + 8 < p.cols) row_store8(row, c[j] + 1, p.cols, b);
+                }
+                if (c[j] % 16 == 0) p.scales[(size_t)r[j] * p.scale_stride + c[j] / 16] = scale;
+            }
         }
     }
 }
@@ -168,27 +203,24 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantParams p) {
     __shared__ uint32_t part[8];
     const int r0 = blockIdx.y * 128 + (threadIdx.x >> 4), c = blockIdx.x * 16 + (threadIdx.x & 15);
     const bool in = 8 * c < p.cols;
-    Floats8 f[8];
+    Raw8<X> raw[8];
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        f[i] = Floats8{};
-        if (in && r0 + 16 * i < p.rows) f[i] = row_load8<X>(static_cast<const X *>(p.x) + (size_t)(r0 + 16 * i) * p.x_stride, c, p.cols);
-    }
+    for (int i = 0; i < 8; i++)              // (a row behind the last is as one without columns)
+        raw[i] = row_load8<X>(static_cast<const X *>(p.x) + (size_t)min(r0 + 16 * i, p.rows - 1) * p.x_stride, c, r0 + 16 * i < p.rows ? p.cols : 0);
 #pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, most8(f[i].x));
+    for (int i = 0; i < 8; i++) m = max(m, most8(raw[i].floats().x));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; i++) m = max(m, part[i]);
     const float scale = block_scale(m, p.pow2);
-    const float2 inv = inverses(scale);
     if (threadIdx.x == 0) p.scales[(size_t)blockIdx.y * p.scale_stride + blockIdx.x] = scale;
 #pragma unroll
     for (int i = 0; i < 8; i++)
         if (in && r0 + 16 * i < p.rows)
-            row_store8(p.codes + (size_t)(r0 + 16 * i) * p.code_stride, c, p.cols, e4m3_quotients(f[i].x, scale, inv));
+            row_store8(p.codes + (size_t)(r0 + 16 * i) * p.code_stride, c, p.cols, block_codes(raw[i].floats().x, scale, p.pow2));
 }
 
 }  // namespace
@@ -251,8 +283,8 @@ extern "C" int moe_quantise_e4m3(const void *x, int x_dtype, size_t x_stride, in
         return fail(MOE_EINVAL, "%s: rows=%d cols=%d block_rows=%d (1 or %d) pow2=%d", who, rows, cols, block_rows, kScaleBlock, pow2);
     if (x_dtype != MOE_DTYPE_F32 && x_dtype != MOE_DTYPE_BF16) return fail(MOE_EINVAL, "%s: x_dtype=%d", who, x_dtype);
     if (rows == 0 || cols == 0) return MOE_OK;
-    const int blocks = (cols - 1) / kScaleBlock + 1, pairs = (blocks - 1) / 2 + 1, tall = (rows - 1) / kScaleBlock + 1;
-    if ((int64_t)rows * pairs >= (int64_t)1 << 31 || (block_rows != 1 && tall > 65535))
+    const int blocks = (cols - 1) / kScaleBlock + 1, quads = (blocks - 1) / 4 + 1, tall = (rows - 1) / kScaleBlock + 1;
+    if (cols > kMaxCols || (int64_t)rows * quads >= (int64_t)2000000000 || (block_rows != 1 && tall > 65535))
         return fail(MOE_EUNSUPPORTED, "%s: rows=%d cols=%d", who, rows, cols);
     const size_t xe = bytes_of(x_dtype), n = (size_t)rows;
     const Rows in{"x", x, n, cols * xe, x_stride * xe}, out{"codes", codes, n, (size_t)cols, code_stride},
@@ -262,9 +294,9 @@ extern "C" int moe_quantise_e4m3(const void *x, int x_dtype, size_t x_stride, in
     if (int rc = check_rows(who, sc, 4)) return rc;
     if (out.overlaps(in) || sc.overlaps(in) || sc.overlaps(out))
         return fail(MOE_EINVAL, "%s: x, codes and scales overlap", who);
-    const QuantParams p{x, x_stride, code_stride, scale_stride, rows, cols, static_cast<uint8_t *>(codes), scales, pow2 != 0, FastDiv(pairs)};
+    const QuantParams p{x, x_stride, code_stride, scale_stride, rows, cols, static_cast<uint8_t *>(codes), scales, pow2 != 0, FastDiv(quads)};
     if (block_rows == 1) {
-        const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)rows * pairs + 7) / 8, (int64_t)num_sms() * 8);
+        const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)rows * quads + 7) / 8, (int64_t)num_sms() * 8);
         if (x_dtype == MOE_DTYPE_BF16) quant_rows_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p);
         else quant_rows_kernel<float><<<grid, 256, 0, stream>>>(p);
     } else {
