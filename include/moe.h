@@ -189,7 +189,8 @@ int moe_debug_dequant(const void *blob, int d, int F, int bits, int which,
 
 /* Test hook, process-wide: the bound of every device-side wait of the
  * batched tensor-core engine (moe_expert_ffn_int4 and moe_prerouter_head with
- * T > 1 bf16 tokens), timeout_ns (0 = 1 second), read at each launch.
+ * T > 1 bf16 tokens) and of moe_scaled_product (there by counted polls, of
+ * about that time), timeout_ns (0 = 1 second), read at each launch.
  * stall != 0 adds to every later launch one wait for bytes that no copy
  * sends: it runs out after timeout_ns, MOE_ETIMEOUT lands in the call's
  * status word (ws word 0) and the launch returns with invalid outputs.

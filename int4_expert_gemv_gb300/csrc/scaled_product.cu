@@ -94,7 +94,7 @@ __device__ __forceinline__ void wait_on(uint64_t *bar, uint32_t parity, int &lef
 
 // Polls of a whole kernel of n blocks: a wait's, and what waits take that are in time.
 __device__ __forceinline__ int all_polls(uint32_t polls, int n) {
-    return (int)min((uint64_t)polls * 2 + (uint64_t)n * 1024, (uint64_t)INT32_MAX);
+    return (int)min((uint64_t)polls * 2 + (uint64_t)n * 4, (uint64_t)INT32_MAX);
 }
 
 // A place in a ring of n, and the parity of the phase that its next turn is
@@ -614,8 +614,8 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 }
 
 // ---------------------------------------------------------------- host
-// A poll that fails takes some 50 ns, 32 of them asleep.
-uint32_t polls_of(uint64_t ns) { return (uint32_t)std::min<uint64_t>(ns / 50 + 1, INT32_MAX); }
+// The hardware holds a poll that fails for 3.8 us.
+uint32_t polls_of(uint64_t ns) { return (uint32_t)std::min<uint64_t>(ns / 3800 + 1, INT32_MAX); }
 
 int encode_tile(CUtensorMap *m, const void *base, size_t rows, size_t cols, size_t stride, int box_rows) {
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {rows > 1 ? stride : align_up(cols, 16)};

@@ -13,6 +13,11 @@ page plan of each step; PagedDecoder runs whole decode steps of one layer:
             moe_scored_route (sigmoid scores, balance bias, groups)
   experts   moe_expert_ffn_int4, moe_combine_residual
 
+With dense="e4m3" the norms, projections and the rotary embedding go through
+the framework as well, weights and activations in 8 bits with a scale for each
+block of 128: moe_add_rms_norm, moe_scaled_product, moe_rotary,
+moe_quantise_e4m3 (Dense8).
+
 The pages this framework follows predict the route a token ahead
 (moe_prerouter_head, moe_topk_route); this is the layer of a model that routes
 by scores instead, as far as the expert FFN's own calls go.  Weights are
@@ -115,12 +120,69 @@ def rotate(x: torch.Tensor, places: torch.Tensor) -> torch.Tensor:
     return torch.cat([a * c - b * s, b * c + a * s], -1).to(x.dtype)
 
 
+def quantised(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, moe.ScaledMatrixDesc]:
+    """A weight matrix [N][K] (fp32 or bf16) in 8 bits: its codes, the scales of
+    its 128 x 128 blocks, and the descriptor that moe_scaled_product takes
+    (both tensors have to live as long as it is used)."""
+    N, K = w.shape
+    codes = torch.empty((N, -(-K // 16) * 16), dtype=torch.float8_e4m3fn, device=w.device)[:, :K]
+    scales = torch.empty((-(-N // 128), -(-K // 128)), device=w.device)
+    moe.moe_quantise_e4m3(w, N, K, codes, scales, block_rows=128)
+    return codes, scales, moe.ScaledMatrixDesc(N=N, K=K, w=codes.data_ptr(), w_stride=codes.stride(0),
+                                               scales=scales.data_ptr(), scale_stride=scales.stride(0))
+
+
+class Dense8:
+    """The dense half of a decoder layer for R tokens, in 8 bits: w_qkv [d][n]
+    and w_out [Hq * D][d] are laid out once, buffers kept."""
+
+    def __init__(self, R: int, d: int, Hq: int, Hkv: int, D: int, w_qkv: torch.Tensor, w_out: torch.Tensor):
+        dev = w_qkv.device
+        self.R, self.Hq, self.Hkv, self.D = R, Hq, Hkv, D
+        self.qkv_codes, self.qkv_scales, self.qkv_desc = quantised(w_qkv.t().contiguous())
+        self.out_codes, self.out_scales, self.out_desc = quantised(w_out.t().contiguous())
+        self.norm = moe.NormDesc(d=d, eps=1e-6, weight=None, w_dtype=moe.MOE_DTYPE_F32, pow2=0)
+        # the embedding of rotate()
+        self.rope = moe.RotaryDesc(D=D, rot=D, first=0, layout=moe.MOE_ROTARY_HALF, scaling=moe.MOE_ROTARY_PLAIN,
+                                   base=10000.0, amplitude=1.0)
+        self.turns = torch.empty(D // 2, dtype=torch.int64, device=dev)
+        moe.moe_rotary_table(self.rope, self.turns)
+        bf, f32, e4 = (dict(dtype=t, device=dev) for t in (torch.bfloat16, torch.float32, torch.float8_e4m3fn))
+        self.x, self.x_scales = torch.zeros((R, d), **e4), torch.zeros((R, -(-d // 128)), **f32)
+        self.qkv = torch.zeros((R, w_qkv.shape[1]), **bf)
+        self.a, self.a_scales = torch.zeros((R, Hq * D), **e4), torch.zeros((R, -(-Hq * D // 128)), **f32)
+        self.proj, self.h, self.hn = torch.zeros((R, d), **bf), torch.zeros((R, d), **f32), torch.zeros((R, d), **bf)
+        self.ws = torch.zeros(max(moe.moe_scaled_product_workspace_bytes(self.qkv_desc, R),
+                                  moe.moe_scaled_product_workspace_bytes(self.out_desc, R)), dtype=torch.uint8, device=dev)
+
+    def project(self, x: torch.Tensor, at: torch.Tensor) -> torch.Tensor:
+        """q, k and v [R][n] of the residual stream x fp32 [R][d], q and k turned
+        by their places (int32 [R])."""
+        Hq, Hkv, D = self.Hq, self.Hkv, self.D
+        moe.moe_add_rms_norm(self.norm, x, self.R, self.x, scales=self.x_scales)
+        moe.moe_scaled_product(self.qkv_desc, self.x, self.x_scales, self.R, self.qkv, self.ws)
+        q, k = self.qkv[:, : Hq * D], self.qkv[:, Hq * D: (Hq + Hkv) * D]
+        moe.moe_rotary(self.rope, self.turns, at, self.R, q, Hq, q, k, Hkv, k)
+        return self.qkv
+
+    def close(self, x: torch.Tensor, attn: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+        """The residual stream with the attention's output [R][Hq][D] projected
+        and added, and its norm in bf16."""
+        moe.moe_quantise_e4m3(attn, self.R, self.Hq * self.D, self.a, self.a_scales)
+        moe.moe_scaled_product(self.out_desc, self.a, self.a_scales, self.R, self.proj, self.ws)
+        moe.moe_add_rms_norm(self.norm, self.proj, self.R, self.hn, res=x, sum=self.h)
+        return self.h, self.hn
+
+
 class PagedDecoder:
     """Decode steps of one layer over a batch of R requests (bf16 activations,
-    fp32 residual stream)."""
+    fp32 residual stream); dense: the type of the norms' and projections'
+    products, "bf16" (plain torch) or "e4m3" (Dense8)."""
 
     def __init__(self, model: DeviceModel, cache: PagedCache, Hq: int, layer: int = 0, seed: int = 0,
-                 n_group: int = 8, keep_group: int = 4, factor: float = 2.5):
+                 n_group: int = 8, keep_group: int = 4, factor: float = 2.5, dense: str = "bf16"):
+        if dense not in ("bf16", "e4m3"):
+            raise ValueError(f"dense={dense!r}: bf16 or e4m3")
         self.m, self.cache, self.Hq = model, cache, Hq
         c, dev, R = model.cfg, model.device, cache.R
         self.cfg, self.ly = c, model.layers[layer]
@@ -129,6 +191,7 @@ class PagedDecoder:
         n = (Hq + 2 * self.Hkv) * self.D
         w = lambda i, o: (torch.randn((i, o), generator=g, device=dev) * i ** -0.5).bfloat16()  # noqa: E731
         self.w_qkv, self.w_out = w(c.d, n), w(Hq * self.D, c.d)
+        self.dense = Dense8(R, c.d, Hq, self.Hkv, self.D, self.w_qkv, self.w_out) if dense == "e4m3" else None
         self.bias = 0.02 * torch.randn(c.E, generator=g, device=dev)
         self.route = moe.RouteDesc(E=c.E, K=c.K, score=moe.MOE_SCORE_SIGMOID, n_group=n_group,
                                    keep_group=keep_group, group_best=min(2, c.E // n_group),
@@ -155,17 +218,25 @@ class PagedDecoder:
         if rows.numel() > ca.max_new:
             raise ValueError(f"{rows.numel()} tokens in a step of a cache with places for {ca.max_new}")
         ca.plan(new_len, min(R, ca.max_new))
-        xn = (x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)).bfloat16()
-        qkv = xn @ self.w_qkv
-        q = qkv[:, : self.Hq * self.D].view(R, self.Hq, self.D)
         at = (ca.seq_len - 1).clamp(min=0)
-        q = rotate(q, at)
-        k = rotate(qkv[:, self.Hq * self.D: (self.Hq + self.Hkv) * self.D].view(R, self.Hkv, self.D), at)
+        if self.dense is not None:
+            qkv = self.dense.project(x, at)
+            q = qkv[:, : self.Hq * self.D]
+            k = qkv[:, self.Hq * self.D: (self.Hq + self.Hkv) * self.D]
+        else:
+            xn = (x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)).bfloat16()
+            qkv = xn @ self.w_qkv
+            q = qkv[:, : self.Hq * self.D].view(R, self.Hq, self.D)
+            q = rotate(q, at)
+            k = rotate(qkv[:, self.Hq * self.D: (self.Hq + self.Hkv) * self.D].view(R, self.Hkv, self.D), at)
         ca.append(k[rows].flatten(1), qkv[rows, (self.Hq + self.Hkv) * self.D:])
         moe.moe_paged_attention(ca.desc, q, R, self.Hq, ca.seq_len, ca.table, ca.max_blocks,
                                 self.D ** -0.5, self.attn, self.attn_ws)
-        h = x + (self.attn.flatten(1) @ self.w_out).float()
-        hn = (h * torch.rsqrt(h.square().mean(1, keepdim=True) + 1e-6)).bfloat16()
+        if self.dense is not None:
+            h, hn = self.dense.close(x, self.attn)
+        else:
+            h = x + (self.attn.flatten(1) @ self.w_out).float()
+            hn = (h * torch.rsqrt(h.square().mean(1, keepdim=True) + 1e-6)).bfloat16()
         moe.moe_prerouter_head(self.ly["router_desc"], hn, None, None, c.K, R, self.logits, self.head_ws)
         moe.moe_scored_route(self.route, self.logits, R, self.idx, self.w)
         moe.moe_expert_ffn_int4(self.ly["experts_desc"], hn, self.idx, R, c.K, self.y, self.ffn_ws)
@@ -173,9 +244,17 @@ class PagedDecoder:
         self.hidden = h
         return self.out
 
+    def check(self) -> None:
+        """Waits for the GPU; raises MoEError if a plan since the last check did
+        not fit (PagedCache.check), or a product's wait has run out."""
+        self.cache.check()
+        if self.dense is not None and int(self.dense.ws[:4].view(torch.int32)[0]) != moe.MOE_OK:
+            self.dense.ws.zero_()
+            raise moe.MoEError(moe.MOE_ETIMEOUT, "moe_scaled_product", "a wait on the device ran out: the steps since are invalid")
+
 
 def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int = 2, D: int = 128,
-        page: int = 16, dtype=torch.bfloat16) -> dict:
+        page: int = 16, dtype=torch.bfloat16, dense: str = "bf16") -> dict:
     """Requests of up to `length` cached tokens (random), `steps` decode steps
     of one layer, the first three of them untimed where there are more; the
     time of a step in microseconds."""
@@ -185,7 +264,7 @@ def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int 
     model = DeviceModel(cfg, heads=False)
     blocks = (length + steps + 2 * page) // page
     cache = PagedCache(R, R * blocks, page, Hkv, D, blocks, max(R, R * length), dtype, scale=0.01)
-    dec = PagedDecoder(model, cache, Hq)
+    dec = PagedDecoder(model, cache, Hq, dense=dense)
     g = torch.Generator(device="cuda").manual_seed(1)
     have = torch.randint(length // 2 + 1, length + 1, (R,), generator=g, device="cuda", dtype=torch.int32)
     cache.plan(have)
@@ -204,7 +283,7 @@ def run(cfg: MoEConfig, R: int, length: int, steps: int, Hq: int = 16, Hkv: int 
         x = dec.step(x, rows, one).clone()
     ev[1].record()
     torch.cuda.synchronize()
-    cache.check()
+    dec.check()
     return {"requests": R, "cached_tokens": int(cache.seq_len.sum()),
             "us_per_step": ev[0].elapsed_time(ev[1]) * 1e3 / timed}
 
@@ -217,6 +296,8 @@ if __name__ == "__main__":
     ap.add_argument("--length", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--e4m3-dense", action="store_true", help="norms and projections in 8 bits")
     a = ap.parse_args()
     print(run(ALL[a.config], a.requests, a.length, a.steps,
-              dtype=torch.float8_e4m3fn if a.e4m3 else torch.bfloat16))
+              dtype=torch.float8_e4m3fn if a.e4m3 else torch.bfloat16,
+              dense="e4m3" if a.e4m3_dense else "bf16"))

@@ -188,3 +188,9 @@ def test_binding_refuses_types(m):
         m.moe_rotary(m.RotaryDesc(D=128, rot=128), c, c, 2, x, 1, x.bfloat16(), stream=0)
     with pytest.raises(ValueError):
         m.moe_quantise_e4m3(torch.zeros((128, 2)).t(), 2, 128, c, s, stream=0)
+
+
+def test_paged_decoder_refuses_another_dense_type(m):
+    from int4_expert_gemv_gb300 import paged
+    with pytest.raises(ValueError):
+        paged.PagedDecoder(None, None, 4, dense="int8")
