@@ -114,10 +114,12 @@ __global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : NV == 1 ? 256 : 1024) n
     }
 }
 
-// A CTA for a row of each SM's share while they last.
+// The CTAs that the SMs hold, or fewer where there are fewer rows.  (The
+// occupancy takes the host a microsecond: not asked for where it does not count.)
 template <typename F>
 int norm_grid(F kernel, int threads, int64_t rows) {
     int ctas = 1;
+    if (rows <= num_sms()) return (int)rows;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, 0) != cudaSuccess || ctas < 1) ctas = 1;
     return (int)std::min<int64_t>(rows, (int64_t)ctas * num_sms());
 }

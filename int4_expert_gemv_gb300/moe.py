@@ -384,31 +384,45 @@ def moe_paged_attention(kv: KVDesc, q, B: int, Hq: int, seq_len, block_table, ma
                                      _stream(stream)), "moe_paged_attention")
 
 
-def _codes_dtype(t) -> int:
-    """The type of a result that may be in 8 bits."""
-    import torch
-    return MOE_DTYPE_E4M3 if t.dtype in (torch.float8_e4m3fn, torch.uint8) else _dtype_code(t)
+_kinds = None
+
+
+def _kind(t) -> int:
+    """The type of numbers that may be in 8 bits (codes as uint8, too)."""
+    global _kinds
+    if _kinds is None:
+        import torch
+        _kinds = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
+                  torch.float8_e4m3fn: MOE_DTYPE_E4M3, torch.uint8: MOE_DTYPE_E4M3}
+    try:
+        return _kinds[t.dtype]
+    except KeyError:
+        raise TypeError(f"numbers must be float32, bfloat16 or float8_e4m3fn, got {t.dtype}") from None
+
+
+def _stride0(t) -> int:
+    """_row_stride, at once for the rows of a matrix."""
+    st = t.stride()
+    return st[0] if len(st) == 2 and st[1] == 1 else _row_stride(t)
 
 
 def _code_rows(t, what: str) -> int:
-    import torch
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if _kind(t) != MOE_DTYPE_E4M3:
         raise TypeError(f"{what} must be float8_e4m3fn (or uint8), got {t.dtype}")
-    return _row_stride(t)
+    return _stride0(t)
 
 
-def _f32(t, what: str):
-    import torch
-    if t.dtype != torch.float32:
+def _f32(t, what: str) -> int:
+    if _kind(t) != MOE_DTYPE_F32:
         raise TypeError(f"{what} must be float32, got {t.dtype}")
-    return _row_stride(t)
+    return _stride0(t)
 
 
 def moe_quantise_e4m3(x, rows: int, cols: int, codes, scales, block_rows: int = 1,
                       pow2: bool = False, stream=None):
     """x fp32 or bf16 [rows][cols] as e4m3 codes with a fp32 scale for each
     block of block_rows (1 or 128) x 128; rows may be strided."""
-    _check(lib().moe_quantise_e4m3(_ptr(x), _dtype_code(x), _row_stride(x), rows, cols, block_rows,
+    _check(lib().moe_quantise_e4m3(_ptr(x), _dtype_code(x), _stride0(x), rows, cols, block_rows,
                                    int(bool(pow2)), _ptr(codes), _code_rows(codes, "codes"),
                                    _ptr(scales), _f32(scales, "scales"), _stream(stream)),
            "moe_quantise_e4m3")
@@ -418,13 +432,13 @@ def moe_add_rms_norm(nd: NormDesc, x, T: int, y, res=None, sum=None, scales=None
     """y = h / sqrt(mean(h^2) + eps) * weight of h = x + res (res None: x), and
     h itself into sum (of res's type; may be res).  y fp32, bf16 or e4m3 codes
     with their scales; rows may be strided."""
-    yd = _codes_dtype(y)
+    yd = _kind(y)
     if sum is not None and res is not None and sum.dtype != res.dtype:
         raise TypeError(f"sum and res must have one type, got {sum.dtype} and {res.dtype}")
     _check(lib().moe_add_rms_norm(
-        C.byref(nd), _ptr(x), _dtype_code(x), _row_stride(x), _ptr(res),
-        MOE_DTYPE_F32 if res is None else _dtype_code(res), 0 if res is None else _row_stride(res),
-        T, _ptr(sum), 0 if sum is None else _row_stride(sum), _ptr(y), yd, _row_stride(y),
+        C.byref(nd), _ptr(x), _dtype_code(x), _stride0(x), _ptr(res),
+        MOE_DTYPE_F32 if res is None else _dtype_code(res), 0 if res is None else _stride0(res),
+        T, _ptr(sum), 0 if sum is None else _stride0(sum), _ptr(y), yd, _stride0(y),
         _ptr(scales), 0 if scales is None else _f32(scales, "scales"), _stream(stream)),
         "moe_add_rms_norm")
 
@@ -438,7 +452,7 @@ def moe_scaled_product(wd: ScaledMatrixDesc, x, x_scales, T: int, out, ws, strea
     each 128 of a row; ws: zeroed once, its word 0 is the status."""
     _check(lib().moe_scaled_product(C.byref(wd), _ptr(x), _code_rows(x, "x"), _ptr(x_scales),
                                     _f32(x_scales, "x_scales"), T, _ptr(out), _dtype_code(out),
-                                    _row_stride(out), _ptr(ws), _nbytes(ws), _stream(stream)),
+                                    _stride0(out), _ptr(ws), _nbytes(ws), _stream(stream)),
            "moe_scaled_product")
 
 
@@ -452,12 +466,13 @@ def moe_rotary(rd: RotaryDesc, turns, places, T: int, q, Hq: int, q_out, k=None,
     """q and k, [T][H][D] or [T][H * D], fp32 or bf16, turned by their places
     (int32 [T]) into q_out and k_out, which may be q and k; tokens may be
     strided."""
-    one = q if q is not None else k
+    dt = (q if q is not None else k).dtype
     for t in (q, q_out, k, k_out):
-        if t is not None and t.dtype != one.dtype:
-            raise TypeError(f"q, k and their results must have one type, got {one.dtype} and {t.dtype}")
-    row = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
-    _check(lib().moe_rotary(C.byref(rd), _ptr(turns), _ptr(places), T, _dtype_code(one), _ptr(q),
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"q, k and their results must have one type, got {dt} and {t.dtype}")
+    row = lambda t: 0 if t is None else _stride0(t)  # noqa: E731
+    _check(lib().moe_rotary(C.byref(rd), _ptr(turns), _ptr(places), T,
+                            _dtype_code(q if q is not None else k), _ptr(q),
                             row(q), Hq, _ptr(q_out), row(q_out), _ptr(k), row(k), Hk, _ptr(k_out),
                             row(k_out), _stream(stream)), "moe_rotary")
 
