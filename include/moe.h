@@ -425,7 +425,8 @@ typedef struct {
  * before sum is rounded, and is rounded once.  E4M3: codes and the scales of
  * 1 x 128 blocks (scales is read for no other type).  Rows x_stride, ...
  * elements apart, 16-byte multiples (anything for T = 1).  The squares' sum is
- * fp32: rows of numbers above 2^63 overflow it.  A row with NaN is NaN.
+ * fp32: rows of numbers above 2^63 overflow it.  A row with NaN is NaN, and
+ * so is one of zeros with eps 0.
  * sum and y may be x or res themselves (the same address, type and stride);
  * no other overlap of an output. */
 int moe_add_rms_norm(const moe_norm_desc *nd, const void *x, int x_dtype, size_t x_stride,

@@ -44,8 +44,8 @@ __device__ __forceinline__ uint32_t most_of(uint32_t m) {
 // e4m3 codes).  A row belongs to a warp (ROWS warps, each with a row of its
 // own) or, for ROWS = 1, to the CTA; each thread has NV chunks of 8 numbers.
 // Persistent: the next row is on its way while this one is computed.
-template <typename X, typename R, typename Y, int NV, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : NV == 1 ? 256 : 1024) norm_kernel(const NormParams p) {
+template <typename X, typename R, typename Y, int NV, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
     constexpr bool RES = !std::is_void<R>::value, AHEAD = NV < 4;      // (32 numbers and the next 32 do not fit 1024 threads' registers)
     using RT = std::conditional_t<RES, R, float>;
     __shared__ float part[2][32];
@@ -129,11 +129,12 @@ int launch_norm(const NormParams &p, cudaStream_t st) {
     const int chunks = (p.d + 7) / 8;
     auto threads = [&](int nv) { return ((chunks + nv - 1) / nv + 31) / 32 * 32; };
     auto go = [&](auto kernel, int n, int64_t rows) { kernel<<<norm_grid(kernel, n, rows), n, 0, st>>>(p); };
-    if (chunks <= 32) go(norm_kernel<X, R, Y, 1, 4>, 128, (p.T + (int64_t)3) / 4);
-    else if (chunks <= 64) go(norm_kernel<X, R, Y, 2, 4>, 128, (p.T + (int64_t)3) / 4);
-    else if (threads(1) <= 256 && p.T <= 8 * num_sms()) go(norm_kernel<X, R, Y, 1, 1>, threads(1), p.T);
-    else if (threads(2) <= 1024) go(norm_kernel<X, R, Y, 2, 1>, threads(2), p.T);
-    else go(norm_kernel<X, R, Y, 4, 1>, threads(4), p.T);
+    if (chunks <= 32) go(norm_kernel<X, R, Y, 1, 4, 128>, 128, (p.T + (int64_t)3) / 4);
+    else if (chunks <= 64) go(norm_kernel<X, R, Y, 2, 4, 128>, 128, (p.T + (int64_t)3) / 4);
+    else if (threads(1) <= 256 && p.T <= 8 * num_sms()) go(norm_kernel<X, R, Y, 1, 1, 256>, threads(1), p.T);
+    else if (threads(2) <= 512) go(norm_kernel<X, R, Y, 2, 1, 512>, threads(2), p.T);
+    else if (threads(2) <= 1024) go(norm_kernel<X, R, Y, 2, 1, 1024>, threads(2), p.T);
+    else go(norm_kernel<X, R, Y, 4, 1, 1024>, threads(4), p.T);
     return check_launch("norm_kernel");
 }
 

@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
     }
     if (S > 1) {
         cluster_sync();
-        // four rows of a token a thread, in turn among the cluster's threads
+        // four rows of a token a thread, in turn among the cluster's threads (a row a
+        // thread, one load after the other, took half of a call of 256 tokens)
         const uint32_t base = saddr(stages);
         const int items = min(NT, p.T - t0) * 32;
         for (int i = rank * F::kThreads + threadIdx.x; i < items; i += S * F::kThreads) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
 #pragma unroll
             for (int r = 0; r < 8; r++)
                 if (r < S)
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w) : "r"(mapped(base + i * 16, r)));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w) : "r"(mapped(base + i * 16, r)) : "memory");
             float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
             for (int r = 1; r < 8; r++)
@@ -514,7 +515,6 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             if (left <= 0) atomicExch(p.err, MOE_ETIMEOUT);
         }
         __syncwarp();
-        wait(drain_bar, 0, bound);           // what has been issued ends before the memory goes
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManySumRegs));
@@ -606,6 +606,9 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
+    // The last commit's arrival, which the first CTA's MMAs send to both: none is
+    // on its way to a CTA that has gone.
+    if (warp == 9) wait(drain_bar, 0, bound);
     cluster_sync();                      // the other CTA's arrivals and products are done too
     if (warp == 9) {
         tc_fence_after();
@@ -689,7 +692,7 @@ int launch_product(const void *x, size_t x_stride, const moe_scaled_matrix_desc 
     // take 13.7 us in tiles of 128 and 17.8 in tiles of 256, 2048 of 4096 x 4096 39.3 and 32.0.
     const int64_t pairs = std::max(1, num_sms() / 2), rows = (p.T - 1) / 256 + 1;
     auto rounds = [&](int64_t tile) { return (rows * ((p.N - 1) / tile + 1) + pairs - 1) / pairs; };
-    if (rounds(128) * ((int64_t)p.KB + 1) >= INT32_MAX) return fail(MOE_EUNSUPPORTED, "scaled_product: T=%d N=%d K=%d", p.T, p.N, wd->K);
+    if (rounds(128) * ((int64_t)p.KB + 1) >= INT32_MAX || rounds(128) * pairs >= INT32_MAX) return fail(MOE_EUNSUPPORTED, "scaled_product: T=%d N=%d K=%d", p.T, p.N, wd->K);
     return 5 * rounds(128) < 8 * rounds(256) ? launch_many<128, O>(x, x_stride, wd, p, st) : launch_many<256, O>(x, x_stride, wd, p, st);
 }
 

@@ -121,7 +121,7 @@ def rotate(x: torch.Tensor, places: torch.Tensor) -> torch.Tensor:
 
 
 def quantised(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, moe.ScaledMatrixDesc]:
-    """A weight matrix [N][K] (fp32 or bf16) in 8 bits: its codes, the scales of
+    """A weight matrix [N][K] (fp32 or bf16, rows on 16-byte boundaries) in 8 bits: its codes, the scales of
     its 128 x 128 blocks, and the descriptor that moe_scaled_product takes
     (both tensors have to live as long as it is used)."""
     N, K = w.shape
@@ -134,7 +134,8 @@ def quantised(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, moe.ScaledMa
 
 class Dense8:
     """The dense half of a decoder layer for R tokens, in 8 bits: w_qkv [d][n]
-    and w_out [Hq * D][d] are laid out once, buffers kept."""
+    and w_out [Hq * D][d] are laid out once.  What project() and close() return
+    are buffers that the next call writes again."""
 
     def __init__(self, R: int, d: int, Hq: int, Hkv: int, D: int, w_qkv: torch.Tensor, w_out: torch.Tensor):
         dev = w_qkv.device
