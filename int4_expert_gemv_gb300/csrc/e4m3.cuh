@@ -160,7 +160,7 @@ __device__ __forceinline__ void row_store8(uint8_t *row, int c, int n, uint2 w) 
 // scale of 2^-100 to 2^120 nothing underflows that an e4m3 border depends on.
 // (Two products that bracket the quotient and a division where they differ, as
 // the cache's append has it, cost more here: numbers of bf16 over a scale out of
-// bf16 fall on the middle of two codes often.  16381 x 4096: 65 us, this way 46.)
+// bf16 fall on the middle of two codes often.  16381 x 4096: 65 us, this way 50.)
 __device__ __forceinline__ uint2 block_codes(const float *f, float scale, bool pow2) {
     if (pow2) return e4m3x8(f, __uint_as_float(0x7f000000u - __float_as_uint(scale)));       // (NaN from NaN: 0xff000001)
     const float inv = __fdiv_rn(1.0f, scale);

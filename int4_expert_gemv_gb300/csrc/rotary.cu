@@ -6,7 +6,14 @@
 // without what is whole, exact but for F's own rounding (a place of 2^20 times
 // 2^-53 of a turn), at any distance and for negative places too.  Its top two
 // bits, rounded, are the quarter; what is left is within 1/8 of a turn, where
-// fp32 holds it to 2^-27 of itself.  No reduction of a large argument is left.
+// fp32 holds it to 2^-24 of itself.  No reduction of a large argument is left.
+//
+// Bytes bound it where there are many tokens: 16381 tokens of 40 heads of 128
+// take 53 us from bf16 to bf16, 93 % of the copy rate, 8000 in fp32 50 us, 96 %.
+// A token's cosines and sines are made once for all its heads.  Heads whose
+// parts are no multiples of 16 bytes go number by number (4000 tokens of 16 heads of
+// 80 of which 20 turn: 18 us, 17 %), and with few heads of 256 the table is a
+// large part of a CTA's work (4000 tokens of 18: 25 us, 43 %).
 #include <algorithm>
 #include <cmath>
 

@@ -369,20 +369,32 @@ __global__ void __launch_bounds__(Few<MAXN>::kThreads) few_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- many tokens
-// A pair of CTAs computes 256 tokens x 256 outputs: the tokens are the rows of
-// cta_group::2 MMAs (128 in each CTA's TMEM), so that a token's scale belongs
-// to a thread and a weight's to a whole warp, and each CTA brings the tiles of
-// its 128 tokens and of 128 of the outputs (a CTA of its own would have to
-// bring both halves: 48 KB a block of K instead of 32).  Two accumulators of 256 columns
-// fill TMEM, each in two halves that are multiplied, read and freed by themselves (an accumulator's turn,
-// from one block's products to the next one's, is the shorter); eight warps keep 128 sums a thread.  Persistent over the tiles,
-// eight rows of tiles at a time, so that the tiles in work share what L2 holds.
-template <int TILE>                       // outputs of a tile: 256 or 128
+// A pair of CTAs computes 256 tokens x 256 outputs (or 192, or 128): the tokens
+// are the rows of cta_group::2 MMAs (128 in each CTA's TMEM), so that a token's
+// scale belongs to a thread and a weight's to a whole warp, and each CTA brings
+// the tiles of its 128 tokens and of half of the outputs (a CTA of its own would
+// have to bring both halves: 48 KB a block of K instead of 32).  Two
+// accumulators of 256 columns fill TMEM, each in two halves that are multiplied,
+// read and freed by themselves (an accumulator's turn, from one block's products
+// to the next one's, is the shorter); eight warps keep 128 sums a thread.
+// Persistent over the tiles, eight rows of tiles at a time, so that the tiles in
+// work share what L2 holds.
+//
+// 8190 x 5120 x 4096 takes 128 us: 2690 TFLOP/s, 1.4 times the measured rate in
+// bf16.  Its floor is 90 us at twice that rate.  The sums bound it: a block of K takes 710 to 850 clocks where its MMAs take 513;
+// without the sums it takes 105 us, without the scales' loads 123, and a block's
+// 128 x 256 numbers of TMEM read and added by eight warps alone take 360 to 400
+// clocks.  Sixteen warps with 64 sums a thread took 172 us, packed pairs of sums 164.
+template <int TILE>                       // outputs of a tile: 256, 192 or 128
 struct Many {
-    static constexpr int kParts = TILE / 128;                // an MMA's outputs are 128
-    static constexpr int kDepth = 512 / TILE;                // accumulators
+    static constexpr int kParts = TILE > 128 ? 2 : 1;        // MMAs of a step
+    static constexpr int kPart = TILE / kParts;              // outputs of one
+    static constexpr int kDepth = 4 / kParts;                // accumulators, of kParts times 128 columns
     static constexpr int kStage = (128 + TILE / 2) * 128;
-    static constexpr int kStages = TILE == 256 ? 5 : 6;
+    static constexpr int kStages = TILE == 128 ? 6 : 5;
+    // Bytes of a row of the boxes that a warp's TILE / 2 outputs go in.
+    template <typename O>
+    static constexpr int box_row() { return TILE / 2 * (int)sizeof(O) % 128 ? 64 : 128; }
     static constexpr size_t kSmem = 1024 + kStages * kStage + 8 * 8192 + (2 * kStages + 2 * 4 + 2) * 8 + 16;
 };
 constexpr int kManyBoxes = 8192;         // staging of a warp's results
@@ -478,7 +490,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 tma_pair(stage, &xmap, kb * 128, m * 256 + rank * 128, bar);
 #pragma unroll
                 for (int h = 0; h < P; h++)
-                    tma_pair(stage + (128 + h * 64) * 128, &wmap, kb * 128, n * TILE + h * 128 + rank * 64, bar);
+                    tma_pair(stage + (128 + h * M::kPart / 2) * 128, &wmap, kb * 128, n * TILE + h * M::kPart + rank * (M::kPart / 2), bar);
                 if (++kb == p.KB) {
                     kb = 0;
                     if (++li < mine) many_tile(p, pair + li * pairs, m, n);
@@ -506,7 +518,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; kk++)
-                        mma_e4m3<2>(tmem + (k + h) * 128, a + 2 * kk, b + (h * 64 * 128 >> 4) + 2 * kk, idesc_e4m3(256, 128), kk > 0);
+                        mma_e4m3<2>(tmem + (k + h) * 128, a + 2 * kk, b + (h * (M::kPart / 2) * 128 >> 4) + 2 * kk, idesc_e4m3(256, M::kPart), kk > 0);
                     commit_pair(acc_full + k + h);
                 }
                 commit_pair(empty + r.at);
@@ -536,15 +548,21 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             // rows behind the end have scales of 0, columns those of the last block
             const float *sx = p.sx + (size_t)min(t, p.T - 1) * p.sx_stride;
             const float *sw = p.sw + (size_t)min(n0 >> 7, (p.N - 1) >> 7) * p.sw_stride;
+            // (96 outputs may lie in two blocks of 128: from `edge` on in the next one)
+            const float *sw2 = p.sw + (size_t)min((n0 + H - 1) >> 7, (p.N - 1) >> 7) * p.sw_stride;
+            const int edge = 128 - (n0 & 127);
             float acc[H];
 #pragma unroll
             for (int j = 0; j < H; j++) acc[j] = 0.0f;
             // the scales are loaded a block ahead and multiplied when their block comes
-            float xs = __ldg(sx), ws = __ldg(sw);
+            float xs = __ldg(sx), ws = __ldg(sw), ws2 = H == 96 ? __ldg(sw2) : 0.0f;
             for (int kb = 0; kb < p.KB; kb++, q++) {
                 const int k = P * (q % D) + (P == 2 ? h : 0);
-                const float scale = xs * ws;
-                if (kb + 1 < p.KB) xs = __ldg(sx + kb + 1), ws = __ldg(sw + kb + 1);
+                const float scale = xs * ws, scale2 = xs * ws2;
+                if (kb + 1 < p.KB) {
+                    xs = __ldg(sx + kb + 1), ws = __ldg(sw + kb + 1);
+                    if (H == 96) ws2 = __ldg(sw2 + kb + 1);
+                }
                 wait_on<false>(acc_full + k, (q / D) & 1, left);
                 __syncwarp();
                 tc_fence_after();
@@ -553,15 +571,16 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     uint32_t d[16];
                     umma::tmem_ld_x16(lanes + k * 128 + (P == 2 ? 0 : h * H) + c, d);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) acc[c + j] = fmaf(scale, __uint_as_float(d[j]), acc[c + j]);
+                    for (int j = 0; j < 16; j++) acc[c + j] = fmaf(H == 96 && c >= edge ? scale2 : scale, __uint_as_float(d[j]), acc[c + j]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(free_bar + k * 8) : "memory");
             }
-            // this warp's 32 x 128 results, in boxes of 128 bytes a row whose 16-byte
-            // pieces stand as TMA's 128-byte swizzle has them (no bank conflicts)
-            constexpr int PER = 128 / sizeof(O), ROUND = H / PER < 2 ? 1 : 2;        // columns of a box; boxes at a time
+            // this warp's results, in boxes of 32 rows whose 16-byte pieces stand as TMA's
+            // swizzle has them (no bank conflicts)
+            constexpr int ROW = M::template box_row<O>(), PER = ROW / (int)sizeof(O);      // a box's row: bytes, columns
+            constexpr int ROUND = H / PER % 2 ? 1 : 2;                                     // boxes at a time
             const int whole = p.N & ~(16 / (int)sizeof(O) - 1);
             const int t_warp = t - lane;
 #pragma unroll
@@ -571,7 +590,7 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                 for (int b = 0; b < ROUND; b++)
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
+                    for (int i = 0; i < ROW / 16; i++) {
                         uint4 w;
                         float f[8];
 #pragma unroll
@@ -581,14 +600,14 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                         }
                         if constexpr (sizeof(O) == 2) w = bf16x8(f);
                         else w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-                        *reinterpret_cast<uint4 *>(box + b * 4096 + lane * 128 + ((i ^ (lane & 7)) << 4)) = w;
+                        *reinterpret_cast<uint4 *>(box + b * 32 * ROW + lane * ROW + ((i ^ (ROW == 128 ? lane & 7 : lane >> 1 & 3)) << 4)) = w;
                     }
                 umma::fence_async_shared();
                 __syncwarp();
                 if (lane == 0 && t_warp < p.T) {
 #pragma unroll
                     for (int b = 0; b < ROUND; b++)
-                        if (n0 + c + b * PER < whole) tma_store(&omap, box + b * 4096, n0 + c + b * PER, t_warp);
+                        if (n0 + c + b * PER < whole) tma_store(&omap, box + b * 32 * ROW, n0 + c + b * PER, t_warp);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
@@ -632,10 +651,11 @@ template <int TILE, typename O>
 int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd, const ProductParams &q, cudaStream_t st) {
     CUtensorMap xmap, wmap, omap;
     const cuuint64_t dims[2] = {std::max<cuuint64_t>(16 / sizeof(O), q.N / (16 / sizeof(O)) * (16 / sizeof(O))), (cuuint64_t)q.T}, strides[1] = {(q.T > 1 ? q.out_stride : align_up(q.N, 8)) * sizeof(O)};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(O)), 32};
-    if (encode_tile(&xmap, x, q.T, wd->K, x_stride, 128) || encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, 64) ||
+    constexpr int row = Many<TILE>::template box_row<O>();
+    const cuuint32_t box[2] = {(cuuint32_t)(row / sizeof(O)), 32};
+    if (encode_tile(&xmap, x, q.T, wd->K, x_stride, 128) || encode_tile(&wmap, wd->w, wd->N, wd->K, wd->w_stride, Many<TILE>::kPart / 2) ||
         pipe::encode_map(&omap, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q.out, dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
+                         row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return no_map();
     static OnDevices ready;
     const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<TILE, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Many<TILE>::kSmem); });
@@ -687,13 +707,17 @@ int launch_product(const void *x, size_t x_stride, const moe_scaled_matrix_desc 
         if (p.nt <= 32) return launch_few<32, O>(x, x_stride, wd, p, st);
         return launch_few<64, O>(x, x_stride, wd, p, st);
     }
-    // Pairs' tiles by the rounds that the grid takes over them, a round of 128 outputs
-    // for five eighths of one of 256 (32 blocks of K: 9.9 and 16.0 us): 256 tokens of 5120 x 4096
-    // take 13.7 us in tiles of 128 and 17.8 in tiles of 256, 2048 of 4096 x 4096 39.3 and 32.0.
+    // Pairs' tiles by the rounds that the grid takes over them: a round of 128
+    // outputs takes 16.3 us over 64 blocks of K, one of 192 20.8, one of 256 24.5, beside
+    // some 5 us of a call.  256 tokens of 5120 x 4096 take 13.7 us in tiles of 128
+    // and 17.8 in tiles of 256, 505 of 5000 x 4000 21.8, 16.0 (192) and 17.8,
+    // 2048 of 4096 x 4096 39.3 and 32.0.
     const int64_t pairs = std::max(1, num_sms() / 2), rows = (p.T - 1) / 256 + 1;
     auto rounds = [&](int64_t tile) { return (rows * ((p.N - 1) / tile + 1) + pairs - 1) / pairs; };
     if (rounds(128) * ((int64_t)p.KB + 1) >= INT32_MAX || rounds(128) * pairs >= INT32_MAX) return fail(MOE_EUNSUPPORTED, "scaled_product: T=%d N=%d K=%d", p.T, p.N, wd->K);
-    return 5 * rounds(128) < 8 * rounds(256) ? launch_many<128, O>(x, x_stride, wd, p, st) : launch_many<256, O>(x, x_stride, wd, p, st);
+    const int64_t c128 = 10 * rounds(128), c192 = 13 * rounds(192), c256 = 15 * rounds(256);
+    if (c128 <= c192 && c128 <= c256) return launch_many<128, O>(x, x_stride, wd, p, st);
+    return c192 <= c256 ? launch_many<192, O>(x, x_stride, wd, p, st) : launch_many<256, O>(x, x_stride, wd, p, st);
 }
 
 int check_matrix(const moe_scaled_matrix_desc *wd, const char *who) {

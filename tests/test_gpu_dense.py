@@ -328,7 +328,7 @@ def test_product(m, T, N, K, out_type):
 
 @pytest.mark.parametrize("T,N,K,out_type", [
     (1, 2560, 2048, BF16), (1, 5120, 4096, F32), (1, 100, 16384, F32), (3, 8192, 1024, BF16), (40, 2048, 7168, F32), (64, 5120, 4096, BF16),
-    (200, 2560, 2048, BF16), (300, 5000, 4000, F32), (513, 1100, 3000, BF16), (1000, 4096, 1024, F32), (1025, 2560, 2176, BF16), (2048, 2048, 2048, F32),
+    (200, 2560, 2048, BF16), (300, 5000, 4000, F32), (500, 5001, 600, BF16), (513, 1100, 3000, BF16), (1000, 4096, 1024, F32), (1025, 2560, 2176, BF16), (2048, 2048, 2048, F32),
     (3000, 1300, 500, BF16), (4097, 640, 256, F32), (1, 70000, 128, BF16), (70000, 16, 128, F32), (5, 16, 65536, F32), (600, 300, 20000, F32)])
 def test_product_of_larger_sizes(m, T, N, K, out_type):
     _check_product(m, T, N, K, out_type, seed=T + N + K)
