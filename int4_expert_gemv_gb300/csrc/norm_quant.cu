@@ -130,7 +130,8 @@ template <typename F>
 int norm_grid(F kernel, int threads, int64_t rows) {
     int ctas = 1;
     if (rows <= num_sms()) return (int)rows;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, 0) != cudaSuccess || ctas < 1) ctas = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, 0) != cudaSuccess) cudaGetLastError();
+    ctas = std::max(ctas, 1);
     return (int)std::min<int64_t>(rows, (int64_t)ctas * num_sms());
 }
 

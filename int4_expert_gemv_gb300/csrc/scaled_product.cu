@@ -645,6 +645,12 @@ int encode_tile(CUtensorMap *m, const void *base, size_t rows, size_t cols, size
     return pipe::encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// An error of the runtime, which the next launch's check is not to find again.
+int failed(cudaError_t e) {
+    cudaGetLastError();
+    return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
+}
+
 int no_map() { return fail(MOE_ECUDA, "scaled_product: no tensor map"); }
 
 template <int TILE, typename O>
@@ -659,7 +665,7 @@ int launch_many(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd
         return no_map();
     static OnDevices ready;
     const cudaError_t e = ready.once([] { return cudaFuncSetAttribute(many_kernel<TILE, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Many<TILE>::kSmem); });
-    if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return failed(e);
     const ManyParams p{q.sx, q.sw, q.sx_stride, q.sw_stride, q.out_stride, q.T, q.N, q.KB, (q.T - 1) / 256 + 1, (q.N - 1) / TILE + 1, q.out, q.err, q.polls, q.stall};
     const int pairs = (int)std::min<int64_t>(num_sms() / 2, (int64_t)p.tiles_m * p.tiles_n);
     many_kernel<TILE, O><<<2 * pairs, kManyThreads, Many<TILE>::kSmem, st>>>(xmap, wmap, omap, p);
@@ -680,7 +686,7 @@ int launch_few(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd,
     p.stages = std::max(least, std::min({few_share(p.KB, p.split), kFewMaxStages, (100 << 10) / stage}));
     static OnDevices ready;
     cudaError_t e = ready.once([] { return cudaFuncSetAttribute(few_kernel<MAXN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10); });
-    if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return failed(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(Few<MAXN>::kThreads);
@@ -693,7 +699,7 @@ int launch_few(const void *x, size_t x_stride, const moe_scaled_matrix_desc *wd,
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, few_kernel<MAXN, O>, wmap, xmap, p);
-    if (e != cudaSuccess) return fail(MOE_ECUDA, "scaled_product: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return failed(e);
     return check_launch("few_kernel");
 }
 

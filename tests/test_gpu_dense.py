@@ -544,3 +544,45 @@ def test_rotary_of_unaligned_tokens(m):
             m.moe_rotary(rd, turns, places, T, x, H, a)
             m.moe_rotary(rd, turns, places, T, y, H, b)
             assert torch.equal(a, b)
+
+
+FIRST_CALLS = """
+import torch
+from int4_expert_gemv_gb300 import moe, paged
+T, d = %d, 512
+x, places = torch.randn((T, d), device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+w = torch.randn((300, d), device="cuda")
+codes, scales = torch.zeros((300, d), dtype=torch.uint8, device="cuda"), torch.zeros((3, 4), device="cuda")
+desc = moe.ScaledMatrixDesc(N=300, K=d, w=codes.data_ptr(), w_stride=d, scales=scales.data_ptr(), scale_stride=4)
+xc, xs = torch.zeros((T, d), dtype=torch.uint8, device="cuda"), torch.zeros((T, 4), device="cuda")
+out, ws = torch.zeros((T, 304), device="cuda")[:, :300], torch.zeros(256, dtype=torch.uint8, device="cuda")
+rd = moe.RotaryDesc(D=64, rot=64, first=0, layout=0, scaling=0, base=10000.0, amplitude=1.0)
+turns, turned = torch.zeros(32, dtype=torch.int64, device="cuda"), torch.zeros((T, d), device="cuda")
+def calls():
+    moe.moe_quantise_e4m3(w, 300, d, codes, scales, block_rows=128)
+    moe.moe_add_rms_norm(moe.NormDesc(d=d, eps=1e-6, weight=None, w_dtype=0, pow2=0), x, T, xc, scales=xs)
+    moe.moe_scaled_product(desc, xc, xs, T, out, ws)
+    moe.moe_rotary_table(rd, turns)
+    moe.moe_rotary(rd, turns, places, T, x, 8, turned)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+got = out.clone(), turned.clone()
+out.zero_(), turned.zero_()
+calls()
+torch.cuda.synchronize()
+assert torch.equal(got[0], out) and torch.equal(got[1], turned) and float(out.abs().sum()) > 0 and int(ws.view(torch.int32)[0]) == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_first_calls_of_a_process_may_be_captured(T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS % T], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
