@@ -498,6 +498,10 @@ many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             }
         }
         q = __reduce_max_sync(0xffffffffu, (unsigned)q);
+        // A wait has run out: the two CTAs may have asked for different fills, and only
+        // the first one's barriers tell of them.  What is on its way lands meanwhile.
+        if (q < nq)
+            for (int i = 0; i < 64; i++) __nanosleep(1000);
         // the last fill of each stage, the other CTA's part too, lands before the pair exits
         for (int s = 0; rank == 0 && s < M::kStages && s < q; s++) {
             const int last = q - 1 - ((q - 1 - s) % M::kStages);
